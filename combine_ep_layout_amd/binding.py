@@ -30,13 +30,15 @@ EP_FP4X2 = 3
 EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 64
 EP_LAYOUT_SCRATCH_BYTES = 8 << 20
+EP_MOE_MAX_ENTRIES = 1024
 
 SYMBOLS = ("ep_layout_workspace_bytes", "ep_layout", "ep_dispatch", "ep_layout_dispatch",
            "ep_combine",
            "ep_dispatch_compact", "ep_layout_dispatch_compact", "ep_combine_compact",
            "ep_zero_padding", "ep_set_workgroup_limit",
            "ep_get_workgroup_limit", "ep_last_error", "ep_supported", "ep_layout_noalloc",
-           "ep_layout_dispatch_workspace_bytes")
+           "ep_layout_dispatch_workspace_bytes", "ep_moe_layer", "ep_moe_layer_workspace_bytes",
+           "ep_expert_matvec", "ep_swiglu", "ep_swiglu_backward", "ep_expert_wgrad")
 
 
 class EpError(RuntimeError):
@@ -102,6 +104,18 @@ def lib(path: str = None) -> ctypes.CDLL:
     L.ep_last_error.restype = ctypes.c_char_p
     L.ep_supported.argtypes = [_i32, _i32, _i32, _i32]
     L.ep_supported.restype = ctypes.c_int
+    L.ep_moe_layer_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    L.ep_moe_layer_workspace_bytes.restype = _sz
+    L.ep_moe_layer.argtypes = [_vp] * 8 + [_i32] * 6 + [_vp, _vp, _sz, _vp]
+    L.ep_moe_layer.restype = ctypes.c_int
+    L.ep_expert_matvec.argtypes = [_vp] * 5 + [_i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp]
+    L.ep_expert_matvec.restype = ctypes.c_int
+    L.ep_swiglu.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp]
+    L.ep_swiglu.restype = ctypes.c_int
+    L.ep_swiglu_backward.argtypes = [_vp] * 5 + [_i32, _i64, _i32, _i32, _vp, _vp, _vp]
+    L.ep_swiglu_backward.restype = ctypes.c_int
+    L.ep_expert_wgrad.argtypes = [_vp] * 5 + [_i32, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp]
+    L.ep_expert_wgrad.restype = ctypes.c_int
     if path is None:
         _LIB = L
     return L
@@ -250,3 +264,44 @@ def ep_set_workgroup_limit(stream, max_workgroups):
 
 def ep_get_workgroup_limit(stream) -> int:
     return lib().ep_get_workgroup_limit(_s(stream))
+
+
+def ep_moe_layer_workspace_bytes(num_tokens: int, topk: int, intermediate: int) -> int:
+    return int(lib().ep_moe_layer_workspace_bytes(num_tokens, topk, intermediate))
+
+
+def ep_moe_layer(x, topk_idx, topk_weights, bias, w_in, w_in_scales, w_out, w_out_scales,
+                 num_tokens, hidden, intermediate, topk, num_experts, weight_dtype, out, workspace,
+                 workspace_bytes, stream=None):
+    _check(lib().ep_moe_layer(_p(x), _p(topk_idx), _p(topk_weights), _p(bias), _p(w_in),
+                              _p(w_in_scales), _p(w_out), _p(w_out_scales), num_tokens, hidden,
+                              intermediate, topk, num_experts, weight_dtype, _p(out),
+                              _p(workspace), workspace_bytes, _s(stream)))
+
+
+def ep_expert_matvec(x, w, w_scales, counts, offsets, num_experts, capacity_rows, in_features,
+                     out_features, weight_dtype, y, y_dtype, stream=None):
+    _check(lib().ep_expert_matvec(_p(x), _p(w), _p(w_scales), _p(counts), _p(offsets), num_experts,
+                                  capacity_rows, in_features, out_features, weight_dtype, _p(y),
+                                  y_dtype, _s(stream)))
+
+
+def ep_swiglu(gate_up, counts, offsets, num_experts, capacity_rows, intermediate, dtype, h,
+              checkpoint=None, checkpoint_scales=None, stream=None):
+    _check(lib().ep_swiglu(_p(gate_up), _p(counts), _p(offsets), num_experts, capacity_rows,
+                           intermediate, dtype, _p(h), _p(checkpoint), _p(checkpoint_scales),
+                           _s(stream)))
+
+
+def ep_swiglu_backward(dh, checkpoint, checkpoint_scales, counts, offsets, num_experts,
+                       capacity_rows, intermediate, dtype, d_gate_up, h=None, stream=None):
+    _check(lib().ep_swiglu_backward(_p(dh), _p(checkpoint), _p(checkpoint_scales), _p(counts),
+                                    _p(offsets), num_experts, capacity_rows, intermediate, dtype,
+                                    _p(d_gate_up), _p(h), _s(stream)))
+
+
+def ep_expert_wgrad(dy, x, x_scales, counts, offsets, num_experts, capacity_rows, out_features,
+                    in_features, x_dtype, previous, dw, dw_dtype, stream=None):
+    _check(lib().ep_expert_wgrad(_p(dy), _p(x), _p(x_scales), _p(counts), _p(offsets), num_experts,
+                                 capacity_rows, out_features, in_features, x_dtype, _p(previous),
+                                 _p(dw), dw_dtype, _s(stream)))

@@ -624,3 +624,279 @@ int ep_combine_compact(const void *expert_out, const void *bias, const int32_t *
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------- the experts' operators
+
+namespace {
+
+int check_experts(const char *what, int32_t num_experts) {
+  if (num_experts < 1 || num_experts > EP_MAX_EXPERTS)
+    return fail(EP_EINVAL, "%s: num_experts must be in 1..%d (got %d)", what, EP_MAX_EXPERTS,
+                num_experts);
+  return EP_OK;
+}
+
+// counts and offsets of the expand layout: both, or (one expert) neither.
+int check_segments(const char *what, const int32_t *counts, const int32_t *offsets,
+                   int32_t num_experts, int64_t capacity_rows) {
+  if (int rc = check_experts(what, num_experts)) return rc;
+  if (capacity_rows < 0 || capacity_rows > INT32_MAX)
+    return fail(EP_EINVAL, "%s: capacity_rows must be in 0..2^31-1 (got %lld)", what,
+                (long long)capacity_rows);
+  if ((counts == nullptr) != (offsets == nullptr))
+    return fail(EP_EINVAL, "%s: counts and offsets go together", what);
+  if (counts == nullptr && num_experts != 1)
+    return fail(EP_EINVAL, "%s: %d experts need counts and offsets", what, num_experts);
+  if (!aligned(counts, 4) || !aligned(offsets, 4))
+    return fail(EP_EINVAL, "%s: misaligned pointer (int32 arrays need 4 bytes)", what);
+  return EP_OK;
+}
+
+int check_row_dtype(const char *what, int32_t dtype) {
+  if (dtype == EP_BF16 || dtype == EP_FP32) return EP_OK;
+  return fail(EP_EINVAL, "%s: rows are bf16 or fp32 (got dtype %d)", what, dtype);
+}
+
+// One matrix [rows, width] per expert in `dtype` with its scales.
+int check_weights(const char *what, const char *name, const void *w, const float *scales,
+                  int32_t dtype, int64_t rows, int64_t width) {
+  if (dtype != EP_BF16 && dtype != EP_FP8_E4M3 && dtype != EP_FP4X2)
+    return fail(EP_EINVAL, "%s: weights are bf16, fp8 or fp4x2 (got dtype %d)", what, dtype);
+  if (dtype == EP_BF16) {
+    if (scales != nullptr) return fail(EP_EINVAL, "%s: bf16 weights have no scales", what);
+    if (width % 8 != 0)
+      return fail(EP_EINVAL, "%s: rows of %s must be a multiple of 16 bytes (%lld values)", what,
+                  name, (long long)width);
+  } else {
+    if (scales == nullptr) return fail(EP_EINVAL, "%s: %s needs its scales", what, name);
+    if (width % 128 != 0)
+      return fail(EP_EINVAL, "%s: scales need a multiple of 128 values per row of %s (got %lld)", what,
+                  name, (long long)width);
+  }
+  const int64_t bytes = dtype == EP_BF16 ? rows * width * 2
+                                         : (dtype == EP_FP8_E4M3 ? rows * width : rows * width / 2);
+  if (bytes > INT32_MAX)
+    return fail(EP_EINVAL, "%s: one expert's %s has %lld bytes, 2^31 or more", what, name,
+                (long long)bytes);
+  if (!w) return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+  if (!aligned(w, 16) || !aligned(scales, 4))
+    return fail(EP_EINVAL, "%s: misaligned pointer (weight rows need 16 bytes)", what);
+  return EP_OK;
+}
+
+// Rows of [gate | up], `intermediate` values each.
+int check_swiglu(const char *what, int32_t dtype, int32_t intermediate, bool checkpoint,
+                 const void *codes, const float *scales) {
+  if (int rc = check_row_dtype(what, dtype)) return rc;
+  const int step = checkpoint ? 128 : 8;
+  if (intermediate < 1 || intermediate % step != 0 || intermediate > (1 << 24))
+    return fail(EP_EINVAL, "%s: intermediate must be a positive multiple of %d up to 2^24 (got %d)",
+                what, step, intermediate);
+  if (checkpoint && (!codes || !scales))
+    return fail(EP_EINVAL, "%s: the checkpoint and its scales go together", what);
+  if (!aligned(codes, 16) || !aligned(scales, 4))
+    return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+  return EP_OK;
+}
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
+  const char *p = (const char *)a, *q = (const char *)b;
+  return a != nullptr && b != nullptr && p < q + bn && q < p + an;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ep_moe_layer_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t intermediate) {
+  try {
+    if (num_tokens < 0 || topk < 1 || topk > EP_MAX_TOPK || intermediate < 1 ||
+        (int64_t)num_tokens * topk > EP_MOE_MAX_ENTRIES)
+      return 0;
+    return ep::moe_layer_workspace(num_tokens, topk, intermediate);
+  } catch (...) {
+    return 0;
+  }
+}
+
+int ep_moe_layer(const void *x, const int32_t *topk_idx, const float *topk_weights,
+                 const void *bias, const void *w_in, const float *w_in_scales, const void *w_out,
+                 const float *w_out_scales, int32_t num_tokens, int32_t hidden,
+                 int32_t intermediate, int32_t topk, int32_t num_experts, int32_t weight_dtype,
+                 void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  try {
+    const char *what = "ep_moe_layer";
+    discard_stale_error();
+    if (int rc = check_topk(what, num_tokens, topk)) return rc;
+    if (int rc = check_experts(what, num_experts)) return rc;
+    if ((int64_t)num_tokens * topk > EP_MOE_MAX_ENTRIES)
+      return fail(EP_EUNSUPPORTED, "%s: %d tokens x top-%d are more than %d entries", what, num_tokens,
+                  topk, EP_MOE_MAX_ENTRIES);
+    if (hidden < 8 || hidden % 8 != 0)
+      return fail(EP_EINVAL, "%s: token bytes must be a positive multiple of 16 (hidden %d)", what,
+                  hidden);
+    if (intermediate < 8 || intermediate % 8 != 0)
+      return fail(EP_EINVAL, "%s: intermediate must be a positive multiple of 8 (got %d)", what,
+                  intermediate);
+    if (int rc = check_weights(what, "w_in", w_in, w_in_scales, weight_dtype,
+                               2 * (int64_t)intermediate, hidden))
+      return rc;
+    if (int rc = check_weights(what, "w_out", w_out, w_out_scales, weight_dtype, hidden, intermediate))
+      return rc;
+    const int64_t n = (int64_t)num_tokens * topk;
+    if ((int64_t)num_tokens * hidden * 2 > INT32_MAX || n * intermediate * 4 > INT32_MAX)
+      return fail(EP_EINVAL, "%s: token rows of 2^31 bytes or more", what);
+    if (num_tokens > 0 && (!x || !topk_idx || !out || !workspace))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    const size_t need = ep::moe_layer_workspace(num_tokens, topk, intermediate);
+    if (workspace_bytes < need)
+      return fail(EP_EINVAL, "%s: workspace of %zu bytes needed (got %zu)", what, need,
+                  workspace_bytes);
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(bias, 16) || !aligned(workspace, 16) ||
+        !aligned(topk_idx, 4) || !aligned(topk_weights, 4))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows and the workspace need 16 bytes)", what);
+    ep::MoeLayerArgs a{x, topk_idx, topk_weights, bias, w_in, w_in_scales, w_out, w_out_scales,
+                       num_tokens, hidden, intermediate, topk, num_experts, weight_dtype, out,
+                       workspace, (hipStream_t)stream};
+    return from_launch(ep::launch_moe_layer(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_moe_layer: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_moe_layer: unknown exception");
+  }
+}
+
+int ep_expert_matvec(const void *x, const void *w, const float *w_scales, const int32_t *counts,
+                     const int32_t *offsets, int32_t num_experts, int64_t capacity_rows,
+                     int32_t in_features, int32_t out_features, int32_t weight_dtype, void *y,
+                     int32_t y_dtype, void *stream) {
+  try {
+    const char *what = "ep_expert_matvec";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_row_dtype(what, y_dtype)) return rc;
+    if (in_features < 8 || in_features % 8 != 0 || in_features > (1 << 24))
+      return fail(EP_EINVAL, "%s: in_features must be a positive multiple of 8 up to 2^24 (got %d)",
+                  what, in_features);
+    if (out_features < 8 || out_features % 8 != 0)
+      return fail(EP_EINVAL, "%s: out_features must be a positive multiple of 8 (got %d)", what,
+                  out_features);
+    if (int rc = check_weights(what, "w", w, w_scales, weight_dtype, out_features, in_features))
+      return rc;
+    if (capacity_rows > 0 && (!x || !y))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(x, 16) || !aligned(y, 16))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    ep::ExpertMatvecArgs a{x, w, w_scales, counts, offsets, num_experts, capacity_rows, in_features,
+                           out_features, weight_dtype, y, y_dtype == EP_FP32, (hipStream_t)stream};
+    return from_launch(ep::launch_expert_matvec(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_expert_matvec: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_expert_matvec: unknown exception");
+  }
+}
+
+int ep_swiglu(const void *gate_up, const int32_t *counts, const int32_t *offsets,
+              int32_t num_experts, int64_t capacity_rows, int32_t intermediate, int32_t dtype,
+              void *h, void *checkpoint, float *checkpoint_scales, void *stream) {
+  try {
+    const char *what = "ep_swiglu";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_swiglu(what, dtype, intermediate,
+                              checkpoint != nullptr || checkpoint_scales != nullptr, checkpoint,
+                              checkpoint_scales))
+      return rc;
+    if (capacity_rows > 0 && (!gate_up || !h))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(gate_up, 16) || !aligned(h, 16))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    const int64_t bytes = capacity_rows * intermediate * (dtype == EP_FP32 ? 4 : 2);
+    if (overlap(h, bytes, gate_up, 2 * bytes))
+      return fail(EP_EINVAL, "%s: h must not overlap gate_up", what);
+    ep::SwigluArgs a{gate_up, counts, offsets, num_experts, capacity_rows, intermediate,
+                     dtype == EP_FP32, h, checkpoint, checkpoint_scales, (hipStream_t)stream};
+    return from_launch(ep::launch_swiglu(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_swiglu: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_swiglu: unknown exception");
+  }
+}
+
+int ep_swiglu_backward(const void *dh, const void *checkpoint, const float *checkpoint_scales,
+                       const int32_t *counts, const int32_t *offsets, int32_t num_experts,
+                       int64_t capacity_rows, int32_t intermediate, int32_t dtype, void *d_gate_up,
+                       void *h, void *stream) {
+  try {
+    const char *what = "ep_swiglu_backward";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_swiglu(what, dtype, intermediate, capacity_rows > 0, checkpoint,
+                              checkpoint_scales))
+      return rc;
+    if (capacity_rows > 0 && (!dh || !d_gate_up))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(dh, 16) || !aligned(d_gate_up, 16) || !aligned(h, 16))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    const int64_t bytes = capacity_rows * intermediate * (dtype == EP_FP32 ? 4 : 2);
+    if (overlap(d_gate_up, 2 * bytes, dh, bytes) || overlap(d_gate_up, 2 * bytes, h, bytes) ||
+        (h != dh && overlap(h, bytes, dh, bytes)))
+      return fail(EP_EINVAL, "%s: the rows must not overlap (h may be dh)", what);
+    ep::SwigluBackwardArgs a{dh, checkpoint, checkpoint_scales, counts, offsets, num_experts,
+                             capacity_rows, intermediate, dtype == EP_FP32, d_gate_up, h,
+                             (hipStream_t)stream};
+    return from_launch(ep::launch_swiglu_backward(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_swiglu_backward: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_swiglu_backward: unknown exception");
+  }
+}
+
+int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const int32_t *counts,
+                    const int32_t *offsets, int32_t num_experts, int64_t capacity_rows,
+                    int32_t out_features, int32_t in_features, int32_t x_dtype,
+                    const void *previous, void *dw, int32_t dw_dtype, void *stream) {
+  try {
+    const char *what = "ep_expert_wgrad";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_row_dtype(what, dw_dtype)) return rc;
+    if (x_dtype != EP_BF16 && x_dtype != EP_FP8_E4M3)
+      return fail(EP_EINVAL, "%s: rows of x are bf16 or fp8 (got dtype %d)", what, x_dtype);
+    const int step = x_dtype == EP_BF16 ? 8 : 16;
+    if (out_features < 8 || out_features % 8 != 0 || out_features > (1 << 24))
+      return fail(EP_EINVAL, "%s: out_features must be a positive multiple of 8 up to 2^24 (got %d)",
+                  what, out_features);
+    if (in_features < step || in_features % step != 0 || in_features > (1 << 24))
+      return fail(EP_EINVAL, "%s: in_features must be a positive multiple of %d up to 2^24 (got %d)",
+                  what, step, in_features);
+    if (x_scales != nullptr && x_dtype != EP_FP8_E4M3)
+      return fail(EP_EINVAL, "%s: bf16 rows have no scales", what);
+    if (x_scales != nullptr && in_features % 128 != 0)
+      return fail(EP_EINVAL, "%s: scales need a multiple of 128 values per row (got %d)", what,
+                  in_features);
+    if (!dw || (capacity_rows > 0 && (!dy || !x)))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(previous, 16) ||
+        !aligned(x_scales, 4))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    const int64_t bytes =
+        (int64_t)num_experts * out_features * in_features * (dw_dtype == EP_FP32 ? 4 : 2);
+    if (previous != dw && overlap(previous, bytes, dw, bytes))
+      return fail(EP_EINVAL, "%s: previous must be dw itself or not overlap it", what);
+    ep::ExpertWgradArgs a{dy, x, x_scales, counts, offsets, num_experts, capacity_rows,
+                          out_features, in_features, x_dtype == EP_FP8_E4M3, previous, dw,
+                          dw_dtype == EP_FP32, (hipStream_t)stream};
+    return from_launch(ep::launch_expert_wgrad(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_expert_wgrad: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_expert_wgrad: unknown exception");
+  }
+}
+
+}  // extern "C"

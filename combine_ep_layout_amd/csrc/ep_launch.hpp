@@ -1,5 +1,5 @@
 // Host-side interface between the C ABI (ep_capi.cpp) and the kernel
-// launchers (ep_layout.hip, ep_dispatch.hip, ep_combine.hip). Arguments are
+// launchers (the .hip files of this folder). Arguments are
 // validated by the C ABI before any launcher is called.
 #pragma once
 
@@ -94,6 +94,78 @@ struct CompactCombineArgs {
   void *out;
   hipStream_t stream;
   bool fp32 = false;  // binary32 rows (else bf16)
+};
+
+// The experts' operators. dtype: element type of the weights (bf16, or e4m3 /
+// e2m1 pairs with one fp32 scale per 128 values of a row).
+struct MoeLayerArgs {
+  const void *x;
+  const int32_t *topk_idx;
+  const float *topk_weights;
+  const void *bias;
+  const void *w_in;
+  const float *in_scales;
+  const void *w_out;
+  const float *out_scales;
+  int T, H, I, K, E, dtype;
+  void *out;
+  void *workspace;
+  hipStream_t stream;
+};
+
+struct ExpertMatvecArgs {
+  const void *x;
+  const void *w;
+  const float *scales;
+  const int32_t *counts, *offsets;  // both NULL: one expert, every row of the buffer
+  int E;
+  int64_t capacity;
+  int K, N, dtype;  // values per row of x, values per row of y
+  void *y;
+  bool fp32;  // rows of y are binary32 (else bf16)
+  hipStream_t stream;
+};
+
+struct SwigluArgs {
+  const void *gate_up;
+  const int32_t *counts, *offsets;  // both NULL: every row of the buffer
+  int E;
+  int64_t capacity;
+  int I;
+  bool fp32;  // binary32 rows (else bf16)
+  void *h;
+  void *codes;    // NULL: no checkpoint
+  float *scales;
+  hipStream_t stream;
+};
+
+struct SwigluBackwardArgs {
+  const void *dh;
+  const void *codes;
+  const float *scales;
+  const int32_t *counts, *offsets;
+  int E;
+  int64_t capacity;
+  int I;
+  bool fp32;
+  void *d_gate_up;
+  void *h;  // NULL: not recomputed
+  hipStream_t stream;
+};
+
+struct ExpertWgradArgs {
+  const void *dy;
+  const void *x;
+  const float *x_scales;  // NULL with e4m3 rows: scale 1
+  const int32_t *counts, *offsets;
+  int E;
+  int64_t capacity;
+  int N, H;       // columns of dy and of x
+  bool x_fp8;     // rows of x are e4m3 (else bf16)
+  const void *previous;  // NULL: none; may be dw
+  void *dw;
+  bool fp32;      // dw and previous are binary32 (else bf16)
+  hipStream_t stream;
 };
 
 // Launch geometry. By default a grid covers every unit of work with
@@ -198,6 +270,13 @@ int launch_dispatch_compact(const CompactDispatchArgs &a);
 // are the layout's outputs.
 int launch_layout_dispatch_compact(const LayoutArgs &l, const CompactDispatchArgs &d);
 int launch_combine_compact(const CompactCombineArgs &a);
+
+int launch_moe_layer(const MoeLayerArgs &a);
+size_t moe_layer_workspace(int T, int K, int I);
+int launch_expert_matvec(const ExpertMatvecArgs &a);
+int launch_swiglu(const SwigluArgs &a);
+int launch_swiglu_backward(const SwigluBackwardArgs &a);
+int launch_expert_wgrad(const ExpertWgradArgs &a);
 
 bool has_layout(int K);
 bool has_dispatch(int H, int K, int dtype);

@@ -12,6 +12,11 @@
  *                weight them by the router weights, sum in binary32 in k
  *                order, store in the rows' type
  *
+ * between them, the experts' own part: ep_moe_layer (a whole layer for a few
+ * tokens), ep_expert_matvec (products with bf16, 8-bit or 4-bit weights),
+ * ep_swiglu / ep_swiglu_backward (the activation, with an 8-bit checkpoint)
+ * and ep_expert_wgrad (the weight gradient),
+ *
  * and around them: ep_layout_dispatch (layout + dispatch in one launch for a
  * one-tile batch), the non-expand mode (ep_dispatch_compact,
  * ep_combine_compact, ep_layout_dispatch_compact: one row per received
@@ -77,6 +82,9 @@ extern "C" {
 /* Largest expert count and top-k the layout kernels accept. */
 #define EP_MAX_EXPERTS 1024
 #define EP_MAX_TOPK 64
+
+/* Largest num_tokens * topk of ep_moe_layer (128 tokens at top-8). */
+#define EP_MOE_MAX_ENTRIES 1024
 
 /*
  * Bytes of device workspace ep_layout needs for (num_tokens, topk,
@@ -399,6 +407,152 @@ int ep_zero_padding(void *expand_x, int64_t row_bytes, float *expand_scales, int
                     float *expand_weights, const int32_t *counts, const int32_t *offsets,
                     int32_t num_experts, int32_t expert_alignment, int64_t capacity_rows,
                     void *stream);
+
+/*
+ * The experts' operators
+ * ----------------------
+ * What lies between dispatch and combine, on the arrays those two use. Rows
+ * of expert e are [offsets[e], offsets[e] + counts[e]) of an expand buffer of
+ * capacity_rows rows (int32 [E] and [E+1] as written by ep_layout, read on
+ * the device); other rows (alignment padding, the buffer's tail) are neither
+ * read nor written, and the part of a span outside [0, capacity_rows) is
+ * skipped. With one expert, counts and offsets may both be NULL: then every
+ * row of the buffer belongs to it. Shapes are run-time values (no capability
+ * gate); a workgroup cap of the stream applies and changes no result.
+ * Results are a pure function of the inputs. No operand may overlap an
+ * output unless it is said below.
+ *
+ * Weights are one row-major matrix [rows, width] per expert, of dtype
+ *   EP_BF16      bf16, no scales; width a multiple of 8
+ *   EP_FP8_E4M3  e4m3 bytes; width a multiple of 128
+ *   EP_FP4X2     e2m1 pairs, width / 2 bytes a row: the value of even index is
+ *                in a byte's low half; width (counted in values, here and
+ *                below) a multiple of 128
+ * and for the last two one fp32 scale per 128 values of a row, [E, rows,
+ * width / 128]: the weight is code * scale. One expert's matrix is below
+ * 2^31 bytes. Weight products are summed in binary32 per 128 values, the sum
+ * is scaled, and the scaled sums are added in binary32: no weight is rounded.
+ */
+
+/*
+ * Bytes of device workspace ep_moe_layer needs: the list of active experts
+ * and their entries, and 4 * intermediate bytes per (token, k) entry. 0 for
+ * out-of-range arguments (and for no tokens). Scratch: its contents on entry
+ * do not matter; two calls in flight at once (two streams, two graphs that
+ * may replay together) must not share one.
+ */
+size_t ep_moe_layer_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t intermediate);
+
+/*
+ * A whole expert layer for a few tokens (a decode step), in two launches,
+ * without layout, dispatch and combine: per token t and k with e =
+ * topk_idx[t, k] in [0, num_experts) (other ids mask the entry)
+ *   [gate | up] = w_in[e] x[t]          (rows [0, I) of w_in are gate's)
+ *   h           = gate / (1 + exp(-gate)) * up
+ *   out[t]      = sum over k of topk_weights[t, k] * (w_out[e] h)  (+ bias[t])
+ * in binary32 with the k in ascending order, rounded once to bf16; h is
+ * carried as a sum of two bf16 values (2^-17 relative). An id may occur
+ * twice in a token: both entries count. A token without unmasked entries
+ * gets bias[t], or +0.
+ *
+ *   x             bf16 [num_tokens, hidden]
+ *   topk_idx      int32 [num_tokens, topk]
+ *   topk_weights  fp32 [num_tokens, topk], or NULL for 1
+ *   bias          bf16 [num_tokens, hidden] (a shared expert's output, a
+ *                 residual) or NULL; may be out
+ *   w_in          [num_experts, 2 * intermediate, hidden] of weight_dtype
+ *   w_out         [num_experts, hidden, intermediate] of weight_dtype
+ *   out           bf16 [num_tokens, hidden], every row written
+ *   workspace     >= ep_moe_layer_workspace_bytes, 16-byte aligned
+ * hidden and intermediate are multiples of 8 (128 for scaled weights).
+ * Errors: EP_EUNSUPPORTED for num_tokens * topk > EP_MOE_MAX_ENTRIES (use
+ * layout, dispatch, ep_expert_matvec or a grouped product, and combine);
+ * EP_EINVAL otherwise.
+ */
+int ep_moe_layer(const void *x, const int32_t *topk_idx, const float *topk_weights,
+                 const void *bias, const void *w_in, const float *w_in_scales, const void *w_out,
+                 const float *w_out_scales, int32_t num_tokens, int32_t hidden,
+                 int32_t intermediate, int32_t topk, int32_t num_experts, int32_t weight_dtype,
+                 void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Per-expert matrix-vector products for a few rows per expert:
+ *   y[r] = w[e] x[r]  for the rows r of each expert e
+ * summed in binary32, rounded once. Any number of rows is right; beyond
+ * about 64 per expert the weights are read again for every 64.
+ *
+ *   x             bf16 [capacity_rows, in_features], an expand buffer
+ *   w             [num_experts, out_features, in_features] of weight_dtype
+ *   y             [capacity_rows, out_features] of y_dtype (EP_BF16, EP_FP32)
+ * in_features and out_features are multiples of 8 (in_features of 128 for
+ * scaled weights). One dense matrix: num_experts 1 and NULL counts, offsets.
+ * Errors: EP_EINVAL.
+ */
+int ep_expert_matvec(const void *x, const void *w, const float *w_scales, const int32_t *counts,
+                     const int32_t *offsets, int32_t num_experts, int64_t capacity_rows,
+                     int32_t in_features, int32_t out_features, int32_t weight_dtype, void *y,
+                     int32_t y_dtype, void *stream);
+
+/*
+ * The experts' gated activation, and an 8-bit checkpoint of its input for
+ * ep_swiglu_backward. For the experts' rows [gate | up] of gate_up:
+ *   h = gate / (1 + exp(-gate)) * up
+ * in binary32, rounded once to the rows' type; and, unless checkpoint and
+ * checkpoint_scales are NULL, per 128 values of the row the scale 2^p, p the
+ * smallest integer >= -126 that keeps the group's largest finite magnitude
+ * within 448 * 2^p, and the e4m3 codes of value / 2^p (round to nearest
+ * even). An infinity or NaN becomes the code NaN.
+ *
+ *   gate_up             [capacity_rows, 2 * intermediate] of dtype (EP_BF16, EP_FP32)
+ *   h                   [capacity_rows, intermediate] of dtype
+ *   checkpoint          e4m3 [capacity_rows, 2 * intermediate] or NULL
+ *   checkpoint_scales   fp32 [capacity_rows, 2 * intermediate / 128] or NULL
+ * intermediate is a multiple of 128, or without a checkpoint of 8.
+ * Errors: EP_EINVAL.
+ */
+int ep_swiglu(const void *gate_up, const int32_t *counts, const int32_t *offsets,
+              int32_t num_experts, int64_t capacity_rows, int32_t intermediate, int32_t dtype,
+              void *h, void *checkpoint, float *checkpoint_scales, void *stream);
+
+/*
+ * Backward pass of ep_swiglu from its checkpoint: with gate and up = code *
+ * scale, s = 1 / (1 + exp(-gate)), for the experts' rows
+ *   d_gate_up = [dh * up * s * (1 + gate * (1 - s)) | dh * gate * s]
+ *   h         = gate * s * up   (unless h is NULL: for the next weight gradient)
+ * in binary32, rounded once. Any finite fp32 scales are accepted.
+ *
+ *   dh          [capacity_rows, intermediate] of dtype (EP_BF16, EP_FP32)
+ *   d_gate_up   [capacity_rows, 2 * intermediate] of dtype
+ *   h           [capacity_rows, intermediate] of dtype or NULL; may be dh
+ * intermediate is a multiple of 128. Errors: EP_EINVAL.
+ */
+int ep_swiglu_backward(const void *dh, const void *checkpoint, const float *checkpoint_scales,
+                       const int32_t *counts, const int32_t *offsets, int32_t num_experts,
+                       int64_t capacity_rows, int32_t intermediate, int32_t dtype, void *d_gate_up,
+                       void *h, void *stream);
+
+/*
+ * Weight gradient of the experts' products:
+ *   dw[e] = previous[e] + sum over the rows r of expert e of dy[r]^T x[r]
+ * with x kept in bf16 or in 8 bits (rows as dispatch moves them, or a
+ * checkpoint): x[r] = code * x_scales[r], rounded to bf16, which is exact for
+ * power-of-two scales such as ep_swiglu's. Summed in binary32, rounded once.
+ * An expert without rows gets previous[e], or zeros.
+ *
+ *   dy          bf16 [capacity_rows, out_features]
+ *   x           bf16 or e4m3 (x_dtype) [capacity_rows, in_features]
+ *   x_scales    fp32 [capacity_rows, in_features / 128] for e4m3, or NULL (scale 1)
+ *   previous    [num_experts, out_features, in_features] of dw_dtype, NULL
+ *               for zeros, or dw itself (accumulate in place)
+ *   dw          [num_experts, out_features, in_features] of dw_dtype
+ *               (EP_BF16, EP_FP32), every element written
+ * out_features is a multiple of 8; in_features of 8 (bf16), 16 (e4m3) or 128
+ * (with scales). Errors: EP_EINVAL.
+ */
+int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const int32_t *counts,
+                    const int32_t *offsets, int32_t num_experts, int64_t capacity_rows,
+                    int32_t out_features, int32_t in_features, int32_t x_dtype,
+                    const void *previous, void *dw, int32_t dw_dtype, void *stream);
 
 /*
  * CU-limited mode ("MORI JIT v2" section 5.1: geometry buckets prefer the
