@@ -1,5 +1,7 @@
 // The experts' weight gradient on the expand layout for gfx950:
 // dW[e] = sum over the rows r of expert e of dy[r]^T x[r] (+ previous).
+#include <type_traits>
+
 #include "ep_device.hpp"
 #include "ep_launch.hpp"
 
@@ -20,8 +22,10 @@ constexpr int kThreads = 256;
 constexpr int kTileN = 128, kTileH = 256;  // columns of dy and of x per workgroup
 constexpr int kRows = 32;                  // rows of both per step
 constexpr int kStrideY = kTileN * 2 + 32, kStrideX = kTileH * 2 + 64;  // LDS bytes per row
+constexpr int kStrideOut = 64 * 4 + 16;  // 16 rows of 64 results of a wave on their way out
 constexpr int kXcds = 8;
-constexpr uint32_t kOutside = 0x80000000u;
+constexpr uint32_t kOutside = 0x80000000u;  // an offset outside every descriptor
+constexpr int kNonTemporal = 2;             // cache policy of a buffer access
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
   constexpr int kRawBufferFlags = 0x00020000;
@@ -43,79 +47,89 @@ __device__ __forceinline__ bf16x8 column(const char *upper, const char *lower) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// One step's rows on the way from memory to LDS, in a thread's registers.
+// One step's rows on the way from memory to LDS, in a thread's registers: it
+// takes the same 16-byte pieces of every step (two of dy, then those of x), at
+// offsets from the step's first row that are found once per tile.
 template <bool FP8>
 struct Stage {
-  u32x4 y[2], x[FP8 ? 2 : 4];
-  float scale[2];
+  static constexpr int kPiecesX = FP8 ? 2 : 4, kPieces = 2 + kPiecesX;
+  static constexpr int kValues = FP8 ? 16 : 8;  // of x in a piece
+  __amdgpu_buffer_rsrc_t by, bx, bs;
+  uint32_t off[kPieces], off_s[kPiecesX];
+  u32x4 v[2][kPieces];
+  float scale[2][kPiecesX];
+  bool scaled;
 
-  // rows [row, row + rows) of the buffers (rows beyond read as zeros)
-  __device__ __forceinline__ void load(const char *dy, const char *xs, const float *x_scales,
-                                       int64_t row, int rows, int N, int H, int n0, int h0) {
-    const int tid = threadIdx.x;
-    const __amdgpu_buffer_rsrc_t by = buffer_of(dy + row * N * 2, (int64_t)rows * N * 2);
-    const __amdgpu_buffer_rsrc_t bx = buffer_of(xs + row * H * (FP8 ? 1 : 2), (int64_t)rows * H * (FP8 ? 1 : 2));
+  static __device__ __forceinline__ int row_y(int i) { return (threadIdx.x + i * kThreads) / (kTileN / 8); }
+  static __device__ __forceinline__ int col_y(int i) { return (threadIdx.x + i * kThreads) % (kTileN / 8) * 8; }
+  static __device__ __forceinline__ int row_x(int i) { return (threadIdx.x + i * kThreads) / (kTileH / kValues); }
+  static __device__ __forceinline__ int col_x(int i) { return (threadIdx.x + i * kThreads) % (kTileH / kValues) * kValues; }
+
+  __device__ __forceinline__ void place(int N, int H, int n0, int h0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int c = tid + i * kThreads, r = c / (kTileN / 8), n = n0 + c % (kTileN / 8) * 8;
-      y[i] = __builtin_amdgcn_raw_buffer_load_b128(by, (int)(n < N ? ((uint32_t)r * N + n) * 2u : kOutside), 0, 0);
+      const int n = n0 + col_y(i);
+      off[i] = n < N ? ((uint32_t)row_y(i) * N + n) * 2u : kOutside;
     }
-    if constexpr (FP8) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = tid + i * kThreads, r = c / (kTileH / 16), h = h0 + c % (kTileH / 16) * 16;
-        x[i] = __builtin_amdgcn_raw_buffer_load_b128(bx, (int)(h < H ? (uint32_t)r * H + h : kOutside), 0, 0);
-        scale[i] = 1.0f;
-        if (x_scales != nullptr) {
-          const __amdgpu_buffer_rsrc_t bs = buffer_of(x_scales + row * (H / 128), (int64_t)rows * (H / 128) * 4);
-          scale[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-              bs, (int)(h < H ? ((uint32_t)r * (H / 128) + h / 128) * 4u : kOutside), 0, 0));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = tid + i * kThreads, r = c / (kTileH / 8), h = h0 + c % (kTileH / 8) * 8;
-        x[i] = __builtin_amdgcn_raw_buffer_load_b128(bx, (int)(h < H ? ((uint32_t)r * H + h) * 2u : kOutside), 0, 0);
-      }
+    for (int i = 0; i < kPiecesX; ++i) {
+      const int h = h0 + col_x(i);
+      off[2 + i] = h < H ? ((uint32_t)row_x(i) * H + h) * (FP8 ? 1u : 2u) : kOutside;
+      if constexpr (FP8) off_s[i] = h < H ? ((uint32_t)row_x(i) * (H / 128) + h / 128) * 4u : kOutside;
     }
   }
-
-  // 16 bytes of row r; rows 4 to 7 of eight have their 8-byte halves swapped
-  static __device__ __forceinline__ void put_x(char *lx, int r, int h, u32x4 v) {
-    if (r & 4) v = __builtin_shufflevector(v, v, 2, 3, 0, 1);
-    *(u32x4 *)(lx + r * kStrideX + h * 2) = v;
-  }
-  __device__ __forceinline__ void store(char *ly, char *lx) const {
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = tid + i * kThreads;
-      *(u32x4 *)(ly + c / (kTileN / 8) * kStrideY + c % (kTileN / 8) * 16) = y[i];
-    }
+  // The next pieces come from `rows` rows at these addresses; rows beyond read as zeros, and no
+  // rows (the stream's end) touch no memory.
+  __device__ __forceinline__ void aim(const char *y, const char *x, const char *s, int rows, int N,
+                                      int H, bool with_scales) {
+    by = buffer_of(y, (int64_t)(rows * N) * 2);
+    bx = buffer_of(x, (int64_t)(rows * H) * (FP8 ? 1 : 2));
     if constexpr (FP8) {
+      scaled = with_scales;
+      bs = buffer_of(s, scaled ? rows * (H / 128) * 4 : 0);
+    }
+  }
+  __device__ __forceinline__ void load(int set, int i) {
+    v[set][i] = __builtin_amdgcn_raw_buffer_load_b128(i < 2 ? by : bx, (int)off[i], 0, 0);
+    if constexpr (FP8)
+      if (i >= 2) scale[set][i - 2] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs, (int)off_s[i - 2], 0, 0));
+  }
+  // 16 bytes of row r. Rows 4 to 7 of every eight start 8 bytes late, so that the 8-byte pieces
+  // of eight rows that half a wave reads at once lie in different banks.
+  static __device__ __forceinline__ void put_x(char *lx, int r, int h, u32x4 w) {
+    u32x2 *to = (u32x2 *)(lx + r * kStrideX + (r & 4) * 2 + h * 2);
+    to[0] = u32x2{w[0], w[1]};
+    to[1] = u32x2{w[2], w[3]};
+  }
+  __device__ __forceinline__ void store(int set, int i, char *ly, char *lx) const {
+    if (i < 2) {
+      *(u32x4 *)(ly + row_y(i) * kStrideY + col_y(i) * 2) = v[set][i];
+    } else if constexpr (FP8) {
+      const float s = scaled ? scale[set][i - 2] : 1.0f;
+      // A power of two between 2^-64 and 2^64 leaves every value exact in bf16: one instruction
+      // converts two values. Other scales (of any lane of the wave) multiply in binary32 and round.
+      const uint32_t bits = __float_as_uint(s);
+      const bool exact = (bits & 0x807FFFFFu) == 0 && bits >= 0x1F800000u && bits <= 0x5F800000u;
+      u32x4 w[2];
+      if (ballot(!exact) == 0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = tid + i * kThreads, r = c / (kTileH / 16), h = c % (kTileH / 16) * 16;
+        for (int d = 0; d < 4; ++d) {
+          w[d >> 1][(d & 1) * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[set][i][d], s, false));
+          w[d >> 1][(d & 1) * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[set][i][d], s, true));
+        }
+      } else {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          u32x4 w;
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i][half * 2 + d], false);
-            const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)x[i][half * 2 + d], true);
-            w[2 * d] = pack(a[0] * scale[i], a[1] * scale[i]);
-            w[2 * d + 1] = pack(b[0] * scale[i], b[1] * scale[i]);
-          }
-          put_x(lx, r, h + half * 8, w);
+        for (int d = 0; d < 4; ++d) {
+          const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[set][i][d], false);
+          const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[set][i][d], true);
+          w[d >> 1][(d & 1) * 2] = pack(lo[0] * s, lo[1] * s);
+          w[d >> 1][(d & 1) * 2 + 1] = pack(hi[0] * s, hi[1] * s);
         }
       }
+      put_x(lx, row_x(i - 2), col_x(i - 2), w[0]);
+      put_x(lx, row_x(i - 2), col_x(i - 2) + 8, w[1]);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = tid + i * kThreads;
-        put_x(lx, c / (kTileH / 8), c % (kTileH / 8) * 8, x[i]);
-      }
+      put_x(lx, row_x(i - 2), col_x(i - 2), v[set][i]);
     }
   }
 };
@@ -125,92 +139,157 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
     const char *__restrict__ dy, const char *__restrict__ x, const float *__restrict__ x_scales,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int64_t capacity, int N,
     int H, int tiles_h, int tiles, int share, int64_t units, const char *previous, char *dw) {
-  __shared__ __attribute__((aligned(16))) char ly[2][kRows * kStrideY], lx[2][kRows * kStrideX];
+  using Rows = Stage<FP8>;
+  constexpr int kPieces = Rows::kPieces, kElt = FP32 ? 4 : 2;
+  constexpr int kTilesQ = kTileH / 32;  // 16-column tiles of x per wave
+  __shared__ __attribute__((aligned(16))) char lds[2][kRows * (kStrideY + kStrideX)];
+  static_assert(kThreads / kWave * 16 * kStrideOut <= (int)sizeof lds, "the way out fits the steps' LDS");
   const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wn = (wave & 1) * 64, wh = (wave >> 1) * 128;
+  const int wn = (wave & 1) * 64, wh = (wave >> 1) * (kTileH / 2);
   // where this lane's pieces of a step's transposed reads lie: row g * 4 + r16 / 4 (and 16 below it)
   const int row = g * 4 + (r16 >> 2);
   const int at_y = row * kStrideY + wn * 2 + (r16 & 3) * 8;
-  const int at_x = row * kStrideX + wh * 2 + (r16 & 3) * 16, swap = (row & 4) * 2;
+  const int at_x = kRows * kStrideY + row * kStrideX + (row & 4) * 2 + wh * 2 + (r16 & 3) * 16;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    // Workgroup u runs on XCD u % 8: each XCD takes one eighth of every expert's tiles, so what
+    // they share of dy and x is in its own L2, whatever the experts' sizes.
     const int64_t k = u / kXcds;
     const int e = (int)(k / share), t = (int)(u % kXcds) * share + (int)(k % share);
     if (t >= tiles) continue;
     const int n0 = t / tiles_h * kTileN, h0 = t % tiles_h * kTileH;
-    int64_t begin = 0, count = capacity;
+    int64_t begin = 0;
+    int count = (int)capacity;
     if (counts != nullptr) {
-      begin = offsets[e];
-      count = counts[e];
+      begin = __builtin_amdgcn_readfirstlane(offsets[e]);
+      count = __builtin_amdgcn_readfirstlane(counts[e]);
       if (begin < 0 || begin >= capacity || count < 0) count = 0;
-      else if (count > capacity - begin) count = capacity - begin;
+      else if (count > capacity - begin) count = (int)(capacity - begin);
     }
-    f32x4 acc[4][8] = {};
-    Stage<FP8> stage;
-    const auto load = [&](int64_t r0) {
-      stage.load(dy, x, x_scales, begin + r0, (int)(count - r0 < kRows ? count - r0 : kRows), N, H, n0, h0);
-    };
-    if (count > 0) load(0);
-    int buf = 0;
-    __syncthreads();
-    for (int64_t r0 = 0; r0 < count; r0 += kRows, buf ^= 1) {
-      stage.store(ly[buf], lx[buf]);
-      __syncthreads();
-      if (r0 + kRows < count) load(r0 + kRows);
-      bf16x8 b[4];
+    f32x4 acc[4][kTilesQ];
+    if (count > 0) {
+      Rows stage;
+      stage.place(N, H, n0, h0);
+      int left = count;
+      const char *from_y = dy + begin * N * 2, *from_x = x + begin * H * (FP8 ? 1 : 2);
+      const char *from_s = (const char *)(x_scales != nullptr ? x_scales + begin * (H / 128) : nullptr);
+      const auto aim = [&] {  // at the next step
+        stage.aim(from_y, from_x, from_s, left <= 0 ? 0 : (left < kRows ? left : kRows), N, H, x_scales != nullptr);
+        left -= kRows;
+        from_y += (int64_t)kRows * N * 2;
+        from_x += (int64_t)kRows * H * (FP8 ? 1 : 2);
+        if constexpr (FP8) from_s += (int64_t)kRows * (H / 128) * 4;
+      };
+      // Three steps ahead of the products: two steps on their way into registers, one in the
+      // other half of LDS.
+      aim();
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const char *at = ly[buf] + at_y + p * 32;
-        b[p] = column(at, at + 16 * kStrideY);
+      for (int i = 0; i < kPieces; ++i) stage.load(0, i);
+      aim();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) stage.load(1, i);
+      aim();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        stage.store(0, i, lds[0], lds[0] + kRows * kStrideY);
+        stage.load(0, i);
       }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      __syncthreads();
+      const auto step = [&](auto set, auto first) {  // products of the step in lds[set]
+        aim();
+        const char *sy = lds[set] + at_y, *sx = lds[set] + at_x;
+        char *to = lds[set ^ 1];
         // tile q holds, as row 4a + b, column 32 (q / 2) + 8a + 4 (q % 2) + b: two tiles give a
         // lane eight consecutive columns of a row of the gradient
-        const char *at = lx[buf] + at_x + (q >> 1) * 64 + (((q & 1) * 8) ^ swap);
-        const bf16x8 a = column(at, at + 16 * kStrideX);
+        const auto column_x = [&](int q) {
+          const char *at = sx + (q >> 1) * 64 + (q & 1) * 8;
+          return column(at, at + 16 * kStrideX);
+        };
+        bf16x8 b[4], a[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-          acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[p], acc[p][q], 0, 0, 0);
+        for (int p = 0; p < 4; ++p) b[p] = column(sy + p * 32, sy + p * 32 + 16 * kStrideY);
+        a[0] = column_x(0);
+#pragma unroll
+        for (int q = 0; q < kTilesQ; ++q) {
+          if (q < kTilesQ - 1) a[(q + 1) & 1] = column_x(q + 1);
+          if (q < kPieces) {
+            stage.store(set ^ 1, q, to, to + kRows * kStrideY);
+            stage.load(set ^ 1, q);
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q & 1], b[p], first ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[p][q], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+      };
+      constexpr std::integral_constant<int, 0> even{};
+      constexpr std::integral_constant<int, 1> odd{};
+      step(even, std::true_type());
+      for (int rows = count - kRows; rows > 0; rows -= 2 * kRows) {
+        step(odd, std::false_type());
+        if (rows > kRows) step(even, std::false_type());
       }
+    } else {
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int q = 0; q < kTilesQ; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    // Results leave as whole 128-byte lines: 16 rows of 64 columns at a time pass through LDS
+    // (each wave its own part), from where 8 (bf16) or 16 lanes take a row.
+    char *const mine = lds[0] + wave * 16 * kStrideOut;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const int n = n0 + wn + p * 16 + r16;
-      if (n >= N) continue;
+      const int n = n0 + wn + p * 16, rows = N - n < 16 ? N - n : 16;
+      if (rows <= 0) break;
+      const int64_t first = ((int64_t)e * N + n) * H * kElt;
+      const __amdgpu_buffer_rsrc_t to = buffer_of(dw + first, (int64_t)(rows * H) * kElt);
+      const __amdgpu_buffer_rsrc_t old = buffer_of(previous != nullptr ? previous + first : nullptr,
+                                                   previous != nullptr ? (int64_t)(rows * H) * kElt : 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // eight columns at a time
-        const int h = h0 + wh + q * 32 + g * 8;
-        if (h >= H) continue;
-        const int64_t at = ((int64_t)e * N + n) * H + h;
-        f32x4 lo = acc[p][2 * q], hi = acc[p][2 * q + 1];
-        if constexpr (FP32) {
-          if (previous != nullptr) {
-            lo += *(const f32x4 *)(previous + at * 4);
-            hi += *(const f32x4 *)(previous + at * 4 + 16);
-          }
-          *(f32x4 *)(dw + at * 4) = lo;
-          *(f32x4 *)(dw + at * 4 + 16) = hi;
-        } else {
-          if (previous != nullptr) {
-            const u32x4 o = *(const u32x4 *)(previous + at * 2);
+      for (int part = 0; part < kTilesQ / 4; ++part) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              lo[2 * i] += __uint_as_float(o[i] << 16), lo[2 * i + 1] += __uint_as_float(o[i] & 0xFFFF0000u);
-              hi[2 * i] += __uint_as_float(o[2 + i] << 16), hi[2 * i + 1] += __uint_as_float(o[2 + i] & 0xFFFF0000u);
+        for (int q = 0; q < 4; ++q)
+          *(f32x4 *)(mine + r16 * kStrideOut + (q >> 1) * 128 + g * 32 + (q & 1) * 16) = acc[p][part * 4 + q];
+        constexpr int kLanes = FP32 ? 16 : 8, kPasses = 16 * kLanes / kWave;
+        u32x4 was[kPasses];
+        uint32_t off[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int h = h0 + wh + part * 64 + lane % kLanes * (64 / kLanes);
+          off[i] = h < H ? (uint32_t)((i * (kWave / kLanes) + lane / kLanes) * H + h) * kElt : kOutside;
+          if (previous != nullptr) was[i] = __builtin_amdgcn_raw_buffer_load_b128(old, (int)off[i], 0, kNonTemporal);
+        }
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const char *from = mine + (i * (kWave / kLanes) + lane / kLanes) * kStrideOut + lane % kLanes * (256 / kLanes);
+          f32x4 lo = *(const f32x4 *)from;
+          u32x4 w;
+          if constexpr (FP32) {
+            if (previous != nullptr) lo += __builtin_bit_cast(f32x4, was[i]);
+            w = __builtin_bit_cast(u32x4, lo);
+          } else {
+            f32x4 hi = *(const f32x4 *)(from + 16);
+            if (previous != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                lo[2 * j] += __uint_as_float(was[i][j] << 16), lo[2 * j + 1] += __uint_as_float(was[i][j] & 0xFFFF0000u);
+                hi[2 * j] += __uint_as_float(was[i][2 + j] << 16), hi[2 * j + 1] += __uint_as_float(was[i][2 + j] & 0xFFFF0000u);
+              }
             }
+            w = u32x4{pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(hi[0], hi[1]), pack(hi[2], hi[3])};
           }
-          const u32x4 v = {pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(hi[0], hi[1]), pack(hi[2], hi[3])};
-          *(u32x4 *)(dw + at * 2) = v;
+          __builtin_amdgcn_raw_buffer_store_b128(w, to, (int)off[i], 0, kNonTemporal);
         }
       }
     }
+    __syncthreads();
   }
 }
 
-}  // namespace
-
-int launch_expert_wgrad(const ExpertWgradArgs &a) {
+template <bool FP8, bool FP32>
+int wgrad_launch(const ExpertWgradArgs &a) {
   const int cap = stream_workgroup_limit(a.stream);
   const int tn = (a.N + kTileN - 1) / kTileN, th = (a.H + kTileH - 1) / kTileH;
   const int64_t tiles = (int64_t)tn * th;
@@ -219,14 +298,17 @@ int launch_expert_wgrad(const ExpertWgradArgs &a) {
   const int64_t units = (int64_t)a.E * share * kXcds;
   const int64_t most = cap > 0 ? cap : (1 << 23);
   const unsigned blocks = (unsigned)(units < most ? units : most);
-  const auto run = [&](auto kernel) {
-    kernel<<<blocks, kThreads, 0, a.stream>>>((const char *)a.dy, (const char *)a.x, a.x_scales, a.counts,
-                                              a.offsets, a.capacity, a.N, a.H, th, (int)tiles, share,
-                                              units, (const char *)a.previous, (char *)a.dw);
-    return launch_status();
-  };
-  if (a.x_fp8) return a.fp32 ? run(ep_expert_wgrad_tiles<true, true>) : run(ep_expert_wgrad_tiles<true, false>);
-  return a.fp32 ? run(ep_expert_wgrad_tiles<false, true>) : run(ep_expert_wgrad_tiles<false, false>);
+  ep_expert_wgrad_tiles<FP8, FP32><<<blocks, kThreads, 0, a.stream>>>(
+      (const char *)a.dy, (const char *)a.x, a.x_scales, a.counts, a.offsets, a.capacity, a.N, a.H, th,
+      (int)tiles, share, units, (const char *)a.previous, (char *)a.dw);
+  return launch_status();
+}
+
+}  // namespace
+
+int launch_expert_wgrad(const ExpertWgradArgs &a) {
+  if (a.x_fp8) return a.fp32 ? wgrad_launch<true, true>(a) : wgrad_launch<true, false>(a);
+  return a.fp32 ? wgrad_launch<false, true>(a) : wgrad_launch<false, false>(a);
 }
 
 }  // namespace ep
