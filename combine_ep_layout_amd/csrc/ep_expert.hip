@@ -16,6 +16,8 @@
 // nothing is shared between waves, so LDS would only add a trip), and 16
 // tokens as the other; lanes of absent tokens and rows are given an offset
 // outside the buffer descriptor, which reads as 0 and costs no traffic.
+#include <type_traits>
+
 #include "ep_device.hpp"
 #include "ep_launch.hpp"
 
@@ -31,6 +33,7 @@ constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset outside every des
 constexpr int kTile = 16;                   // rows and tokens of one matrix instruction
 constexpr int kStep = 128;                  // values of the long axis per step: one scale group
 constexpr int kThreads = 256;
+constexpr int kWideTiles = 2;               // 16-row tiles per wave of the wide kernels
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
   constexpr int kRawBufferFlags = 0x00020000;
@@ -40,9 +43,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0);
 }
-// Weights are read once: non-temporal.
-__device__ __forceinline__ u32x4 load16_stream(__amdgpu_buffer_rsrc_t b, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 2);
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0));
+}
+
+// Value of `v` held by lane `from` (any lane's choice).
+__device__ __forceinline__ float lane_value(float v, int from) {
+  return __int_as_float(__builtin_amdgcn_ds_bpermute(from * 4, __float_as_int(v)));
 }
 
 // How the values of a step's 128 reach the four matrix instructions of the
@@ -120,89 +127,110 @@ __device__ __forceinline__ Matrix matrix_of(const void *w, const float *scales, 
   return m;
 }
 
-// acc[mt][rt] += rows x tokens over steps [s0, s1). Lane (r = lane % 16,
-// g = lane / 16): row[rt] is its weight row (negative: absent), tok[mt] the
-// byte offset of its token's row in x (kOutside: absent). The tokens are the
-// first operand, so a lane's four results are four tokens of one weight row
-// and it needs one scale. SPLIT: each token row is the sum of two bf16 rows,
-// low_bytes apart (an fp32 value as high and low part).
-template <int WT, int RT, int MT, bool SPLIT>
-__device__ __forceinline__ void multiply(const Matrix &m, const int (&row)[RT],
-                                         __amdgpu_buffer_rsrc_t x, const uint32_t (&tok)[MT],
-                                         uint32_t low_bytes, int s0, int s1,
-                                         f32x4 (&acc)[MT][RT]) {
-  using W = Weights<WT>;
-  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  uint32_t wrow[RT], srow[RT];
-  const int groups = m.width / kStep;
+// Byte offsets of the rows row[rt] (negative: absent) in a matrix and in its scales.
+template <int WT, int RT>
+__device__ __forceinline__ void row_offsets(const Matrix &m, const int (&row)[RT], uint32_t (&wrow)[RT],
+                                            uint32_t (&srow)[RT]) {
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    wrow[rt] = row[rt] < 0 ? kOutside : (uint32_t)(((int64_t)row[rt] * m.width * W::kStepBytes) / kStep);
-    srow[rt] = row[rt] < 0 ? kOutside : (uint32_t)row[rt] * (uint32_t)groups * 4u;
+    const bool in = row[rt] >= 0;
+    wrow[rt] = in ? (uint32_t)(((int64_t)row[rt] * m.width * Weights<WT>::kStepBytes) / kStep) : kOutside;
+    srow[rt] = in ? (uint32_t)row[rt] * (uint32_t)(m.width / kStep) * 4u : kOutside;
   }
-  float ahead[RT];
-#pragma unroll 2
-  for (int s = s0; s < s1; ++s) {
-    u32x4 w[RT][W::kLoads], t[MT][4], low[MT][4];
-    if constexpr (W::kScaled) {
-      // lane group g reads the scale of the g-th of the next four steps
-      if (((s - s0) & 3) == 0) {
+}
+
+// Offset of load l of step s (outside from step s1 on, and behind a row whose
+// width is no multiple of 128).
+template <int WT>
+__device__ __forceinline__ uint32_t weight_at(int width, uint32_t wrow, int s, int s1, int l, int g) {
+  using W = Weights<WT>;
+  const bool in = s < s1 && (W::kScaled || s * kStep + W::place(l, g) < width);
+  return in ? wrow + (uint32_t)s * W::kStepBytes + W::load_byte(l, g) : kOutside;
+}
+
+// acc[rt] += rows x tokens over steps [s0, s1), a wave on its own. Lane
+// (r = lane % 16, g = lane / 16): row[rt] is its weight row (negative:
+// absent), tok the byte offset of its token's row in x (kOutside: absent). The
+// tokens are the first operand, so a lane's four results are four tokens of
+// one weight row and it needs one scale.
+template <int WT, int RT>
+struct Chunk {  // kSteps steps' operands on their way into registers
+  using W = Weights<WT>;
+  static constexpr int kSteps = W::kScaled ? 2 : 1;
+  u32x4 w[kSteps][RT][W::kLoads], t[kSteps][4];
+  float scale[RT];
+
+  // Steps [s, s + kSteps), those from s1 on outside. Lane group g reads the scales of step s + g.
+  __device__ __forceinline__ void load(const Matrix &m, const uint32_t (&wrow)[RT],
+                                       const uint32_t (&srow)[RT], __amdgpu_buffer_rsrc_t x,
+                                       uint32_t tok, int s, int s1) {
+    const int g = lane_id() >> 4;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          ahead[rt] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-              m.scales, (int)(s + g < s1 ? srow[rt] + (uint32_t)(s + g) * 4u : kOutside), 0, 0));
-      }
+    for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int l = 0; l < W::kLoads; ++l)
+          w[u][rt][l] = load16(m.w, weight_at<WT>(m.width, wrow[rt], s + u, s1, l, g));
+    if constexpr (W::kScaled) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        scale[rt] = load4(m.scales, g < kSteps && s + g < s1 ? srow[rt] + (uint32_t)(s + g) * 4u : kOutside);
     }
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int l = 0; l < W::kLoads; ++l) {
-        uint32_t off = wrow[rt] + (uint32_t)s * W::kStepBytes + W::load_byte(l, g);
-        if constexpr (!W::kScaled)  // the last step of a width that is no multiple of 128
-          off = s * kStep + W::place(l, g) < m.width ? off : kOutside;
-        w[rt][l] = load16_stream(m.w, off);
-      }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int u = 0; u < kSteps; ++u)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = s * kStep + W::place(j, g);
-        uint32_t off = tok[mt] + (uint32_t)k * 2u;
-        if constexpr (!W::kScaled) off = k < m.width ? off : kOutside;
-        t[mt][j] = load16(x, off);
-        if constexpr (SPLIT) low[mt][j] = load16(x, off + low_bytes);
+        const int k = (s + u) * kStep + W::place(j, g);
+        const bool in = s + u < s1 && (W::kScaled || k < m.width);
+        t[u][j] = load16(x, in ? tok + (uint32_t)k * 2u : kOutside);
       }
-    f32x4 part[MT][RT];
-    if constexpr (W::kScaled) {
+  }
+
+  __device__ __forceinline__ void add(f32x4 (&acc)[RT]) const {
+    const int r = lane_id() & 15;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) part[mt][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int u = 0; u < kSteps; ++u)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const bf16x8 b = W::operand(w[rt], j);
+        f32x4 sum = acc[rt];
+        if constexpr (W::kScaled) sum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          f32x4 &c = W::kScaled ? part[mt][rt] : acc[mt][rt];
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, t[mt][j]), b, c, 0, 0, 0);
-          if constexpr (SPLIT)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, low[mt][j]), b, c, 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, t[u][j]),
+                                                        W::operand(w[u][rt], j), sum, 0, 0, 0);
+        if constexpr (W::kScaled) {
+          const float sc = lane_value(scale[rt], u * 16 + r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[rt][i] += sc * sum[i];
+        } else {
+          acc[rt] = sum;
         }
       }
-    if constexpr (W::kScaled) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int from = ((((s - s0) & 3) << 4) | r) << 2;
-        const float sc = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(ahead[rt])));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[mt][rt][i] += sc * part[mt][rt][i];
-      }
-    }
+  }
+};
+
+template <int WT, int RT>
+__device__ __forceinline__ void multiply(const Matrix &m, const int (&row)[RT],
+                                         __amdgpu_buffer_rsrc_t x, uint32_t tok, int s0, int s1,
+                                         f32x4 (&acc)[RT]) {
+  constexpr int U = Chunk<WT, RT>::kSteps;
+  uint32_t wrow[RT], srow[RT];
+  row_offsets<WT>(m, row, wrow, srow);
+  // Two chunks in turn: one on its way while the other is used. The barriers keep the compiler
+  // from moving the loads down to their use to save registers.
+  Chunk<WT, RT> a, b;
+  a.load(m, wrow, srow, x, tok, s0, s1);
+  for (int s = s0; s < s1; s += 2 * U) {
+    b.load(m, wrow, srow, x, tok, s + U, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    a.add(acc);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + U >= s1) break;
+    a.load(m, wrow, srow, x, tok, s + 2 * U, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    b.add(acc);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -225,6 +253,133 @@ __device__ __forceinline__ float red_sum(const float *red, int waves, int rt, in
   return v;
 }
 
+// The same product for a workgroup of four waves with different rows and the
+// same tokens, over the whole long axis: the tokens' values come through LDS,
+// loaded once for all four waves, a chunk of 256 bytes of every weight row
+// ahead of the products.
+template <int WT>
+struct WideChunk {
+  using W = Weights<WT>;
+  static constexpr int kSteps = 256 / W::kStepBytes;  // per chunk
+  static constexpr int kValues = kSteps * kStep, kPieces = kValues / 8;  // 16-byte pieces of a token
+  static constexpr int kTokenBytes = kValues * 2;
+};
+template <int WT, int MT>
+constexpr int wide_lds_bytes() {
+  return 2 * MT * kTile * WideChunk<WT>::kTokenBytes;
+}
+
+template <int WT, int RT, int MT>
+__device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[RT],
+                                              __amdgpu_buffer_rsrc_t x, const uint32_t *tok_off,
+                                              char *lds, f32x4 (&acc)[MT][RT]) {
+  using W = Weights<WT>;
+  using C = WideChunk<WT>;
+  constexpr int kMine = MT * kTile * C::kPieces / kThreads;  // pieces per thread
+  const int tid = threadIdx.x, lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int steps = (m.width + kStep - 1) / kStep, chunks = (steps + C::kSteps - 1) / C::kSteps;
+  uint32_t wrow[RT], srow[RT];
+  row_offsets<WT>(m, row, wrow, srow);
+  // A token's pieces are rotated by its number (exclusive or), so that 16 tokens' pieces of the
+  // same place, which 16 lanes read at once, lie in different banks.
+  uint32_t from[kMine];
+  int piece[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int at = tid + i * kThreads, t = at / C::kPieces;
+    piece[i] = (at % C::kPieces) ^ (t & 15);
+    from[i] = tok_off[t] + (uint32_t)piece[i] * 16u;
+  }
+  u32x4 xs[kMine], w[2][C::kSteps][RT][W::kLoads];
+  float scale[2][RT];
+  const auto load_x = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const bool in = W::kScaled ? c < chunks : c * C::kValues + piece[i] * 8 < m.width;
+      xs[i] = load16(x, in ? from[i] + (uint32_t)c * C::kTokenBytes : kOutside);
+    }
+  };
+  const auto store_x = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      *(u32x4 *)(lds + (c & 1) * (MT * kTile * C::kTokenBytes) + (tid + i * kThreads) * 16) = xs[i];
+  };
+  const auto load_w = [&](int c, auto set) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int u = 0; u < C::kSteps; ++u)
+#pragma unroll
+        for (int l = 0; l < W::kLoads; ++l)
+          w[set][u][rt][l] = load16(m.w, weight_at<WT>(m.width, wrow[rt], c * C::kSteps + u, steps, l, g));
+      if constexpr (W::kScaled) {
+        const int s = c * C::kSteps + g;
+        scale[set][rt] = load4(m.scales, g < C::kSteps && s < steps ? srow[rt] + (uint32_t)s * 4u : kOutside);
+      }
+    }
+  };
+  const auto add = [&](int c, auto set) {
+    const char *from_lds = lds + (c & 1) * (MT * kTile * C::kTokenBytes) + r * C::kTokenBytes;
+#pragma unroll
+    for (int u = 0; u < C::kSteps; ++u) {
+      if (u > 0 && c * C::kSteps + u >= steps) break;
+      f32x4 part[MT][RT];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf16x8 t[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          t[mt] = *(const bf16x8 *)(from_lds + mt * kTile * C::kTokenBytes +
+                                    (((u * kStep + W::place(j, g)) / 8) ^ r) * 16);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const bf16x8 b = W::operand(w[set][u][rt], j);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if constexpr (W::kScaled)
+              part[mt][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  t[mt], b, j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : part[mt][rt], 0, 0, 0);
+            else
+              acc[mt][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[mt], b, acc[mt][rt], 0, 0, 0);
+          }
+        }
+      }
+      if constexpr (W::kScaled) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const float sc = lane_value(scale[set][rt], u * 16 + r);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mt][rt][i] += sc * part[mt][rt][i];
+        }
+      }
+    }
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  load_x(0);
+  load_w(0, even);
+  store_x(0);
+  load_x(1);
+  __syncthreads();
+  for (int c = 0; c < chunks; c += 2) {
+    store_x(c + 1);
+    load_x(c + 2);
+    load_w(c + 1, odd);
+    __builtin_amdgcn_sched_barrier(0);
+    add(c, even);
+    __syncthreads();
+    if (c + 1 >= chunks) break;
+    store_x(c + 2);
+    load_x(c + 3);
+    load_w(c + 2, even);
+    __builtin_amdgcn_sched_barrier(0);
+    add(c + 1, odd);
+    __syncthreads();
+  }
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
@@ -234,9 +389,10 @@ __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float
 
 // ------------------------------------------------------------ ep_expert_matvec
 
-// The j-th expert that has rows, by a scan of the counts (1024 at most, four
-// per thread of 256); absent: e = -1. A count is cut to the rows that lie
-// inside the buffer, so no access leaves it whatever the arrays hold.
+// The j-th expert that has rows, found by every wave for itself from the
+// counts (a ballot for every 64 experts); absent: e = -1. A count is cut to
+// the rows that lie inside the buffer, so no access leaves it whatever the
+// arrays hold.
 struct Segment {
   int e;
   int64_t begin, count;
@@ -246,101 +402,134 @@ __device__ __forceinline__ int64_t rows_inside(const int32_t *counts, const int3
   const int64_t b = offsets[e], c = counts[e];
   return b < 0 || b >= capacity ? 0 : (c < capacity - b ? c : capacity - b);
 }
-__device__ __forceinline__ Segment find_segment(int j, const int32_t *counts,
-                                                const int32_t *offsets, int E, int64_t capacity,
-                                                int *lds) {
+__device__ __forceinline__ Segment find_segment(int j, const int32_t *__restrict__ counts,
+                                                const int32_t *__restrict__ offsets, int E,
+                                                int64_t capacity) {
   if (counts == nullptr) return {j == 0 ? 0 : -1, 0, capacity};
-  const int tid = threadIdx.x, wave = tid / kWave;
-  int first = tid * 4, have = 0;
-  if (tid < kThreads)
+  const int lane = lane_id();
+  int e = -1;
+  for (int first = 0; first < E && e < 0; first += 4 * kWave) {
+    uint64_t have[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (first + i < E && rows_inside(counts, offsets, first + i, capacity) > 0) have |= 1 << i;
-  const int mine = __popc(have), upto = wave_inclusive_scan(mine);
-  if (tid == 0) lds[16] = -1;
-  if (lane_id() == kWave - 1) lds[wave] = upto;
-  __syncthreads();
-  int before = upto - mine;
-  for (int w = 0; w < wave; ++w) before += lds[w];
-  if (j >= before && j < before + mine) {
-    int skip = j - before;
+    for (int q = 0; q < 4; ++q) {
+      const int at = first + q * kWave + lane;
+      have[q] = ballot(at < E && rows_inside(counts, offsets, at, capacity) > 0);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (have >> i & 1 && skip-- == 0) lds[16] = first + i;
+    for (int q = 0; q < 4; ++q) {
+      const int n = __builtin_popcountll(have[q]);
+      if (e < 0 && j < n) {
+        const uint64_t hit = ballot((have[q] >> lane & 1) != 0 && count_below(have[q]) == j);
+        e = first + q * kWave + __builtin_ctzll(hit);
+      }
+      j -= n;
+    }
   }
-  __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane(lds[16]);
-  __syncthreads();
   if (e < 0) return {-1, 0, 0};
-  return {e, (int64_t)offsets[e], rows_inside(counts, offsets, e, capacity)};
+  return {e, __builtin_amdgcn_readfirstlane(offsets[e]),
+          __builtin_amdgcn_readfirstlane((int)rows_inside(counts, offsets, e, capacity))};
 }
 
-template <int WT, int RT, int MT, bool FP32>
-__device__ __forceinline__ void matvec_group(const Matrix &m, const uint16_t *x, int64_t row0,
-                                             int rows, int n0, int N, void *y, float *red) {
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int waves = blockDim.x / kWave;
-  const int steps = (m.width + kStep - 1) / kStep;
-  // rows beyond the group lie outside the descriptor
+template <int WT, int MT, bool FP32>
+__device__ __forceinline__ void matvec_wide_group(const Matrix &m, const uint16_t *x, int64_t row0,
+                                                  int rows, int n0, int N, void *y, char *lds,
+                                                  uint32_t *tok_off) {
+  constexpr int RT = kWideTiles;
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const __amdgpu_buffer_rsrc_t xb = buffer_of(x + row0 * m.width, (int64_t)rows * m.width * 2);
+  if (threadIdx.x < MT * kTile)
+    tok_off[threadIdx.x] = (int)threadIdx.x < rows ? threadIdx.x * (uint32_t)m.width * 2u : kOutside;
+  __syncthreads();
   int row[RT];
-  uint32_t tok[MT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    const int n = n0 + rt * kTile + (lane & 15);
+    const int n = n0 + (wave * RT + rt) * kTile + r;
     row[rt] = n < N ? n : -1;
   }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int p = mt * kTile + (lane & 15);
-    tok[mt] = p < rows ? (uint32_t)p * (uint32_t)m.width * 2u : kOutside;
-  }
   f32x4 acc[MT][RT] = {};
-  multiply<WT, RT, MT, false>(m, row, xb, tok, 0, steps * wave / waves, steps * (wave + 1) / waves,
-                              acc);
+  multiply_wide<WT, RT, MT>(m, row, xb, tok_off, lds, acc);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    red_put<RT>(red, wave, acc[mt]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * RT * kTile; i += blockDim.x) {
-      const int c = i % (RT * kTile), p = i / (RT * kTile);
-      const int n = n0 + c;
-      if (mt * kTile + p < rows && n < N) {
-        const float v = red_sum<RT>(red, waves, c / kTile, p, c % kTile);
-        const int64_t at = (row0 + mt * kTile + p) * (int64_t)N + n;
-        if constexpr (FP32) ((float *)y)[at] = v;
-        else ((uint16_t *)y)[at] = bf16_bits(v);
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = mt * kTile + g * 4 + i;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (p >= rows || row[rt] < 0) continue;
+        const int64_t at = (row0 + p) * (int64_t)N + row[rt];
+        if constexpr (FP32) ((float *)y)[at] = acc[mt][rt][i];
+        else ((uint16_t *)y)[at] = bf16_bits(acc[mt][rt][i]);
       }
     }
-    __syncthreads();
-  }
 }
 
-template <int WT, int RT, bool FP32>
-__global__ __launch_bounds__(1024) void ep_expert_matvec_tiles(
+// Many tiles: a workgroup takes 128 rows of one expert's matrix.
+template <int WT, bool FP32>
+__global__ __launch_bounds__(kThreads, 2) void ep_expert_matvec_wide(
     const uint16_t *__restrict__ x, const void *__restrict__ w, const float *__restrict__ scales,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int E,
     int64_t capacity, int K, int N, int64_t units, int tiles, void *__restrict__ y) {
-  extern __shared__ float red[];
-  __shared__ int lds[17];
+  __shared__ __attribute__((aligned(16))) char lds[wide_lds_bytes<WT, 2>()];
+  __shared__ uint32_t tok_off[2 * kTile];
   int have_j = -1;
   Segment seg{-1, 0, 0};
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * RT * kTile;
-    if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity, lds);
+    const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * kWideTiles * kTile * 4;
+    if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
     have_j = j;
     if (seg.e < 0) return;  // no further expert has rows
     const Matrix m = matrix_of<WT>(w, scales, seg.e, N, K);
     for (int64_t p = 0; p < seg.count;) {
       const int64_t left = seg.count - p;
-      const int rows = (int)(left < 4 * kTile ? left : 4 * kTile);
-      if (rows > 2 * kTile)
-        matvec_group<WT, RT, 4, FP32>(m, x, seg.begin + p, rows, n0, N, y, red);
-      else if (rows > kTile)
-        matvec_group<WT, RT, 2, FP32>(m, x, seg.begin + p, rows, n0, N, y, red);
+      const int rows = (int)(left < 2 * kTile ? left : 2 * kTile);
+      if (rows > kTile)
+        matvec_wide_group<WT, 2, FP32>(m, x, seg.begin + p, rows, n0, N, y, lds, tok_off);
       else
-        matvec_group<WT, RT, 1, FP32>(m, x, seg.begin + p, rows, n0, N, y, red);
+        matvec_wide_group<WT, 1, FP32>(m, x, seg.begin + p, rows, n0, N, y, lds, tok_off);
       p += rows;
+    }
+  }
+}
+
+// Few tiles: the 4 to 16 waves of a workgroup share 16 rows' long axis.
+template <int WT, bool FP32>
+__global__ __launch_bounds__(1024) void ep_expert_matvec_split(
+    const uint16_t *__restrict__ x, const void *__restrict__ w, const float *__restrict__ scales,
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int E,
+    int64_t capacity, int K, int N, int64_t units, int tiles, void *__restrict__ y) {
+  extern __shared__ float red[];
+  const int r = lane_id() & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
+  const int steps = (K + kStep - 1) / kStep;
+  int have_j = -1;
+  Segment seg{-1, 0, 0};
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * kTile;
+    if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
+    have_j = j;
+    if (seg.e < 0) return;  // no further expert has rows
+    const Matrix m = matrix_of<WT>(w, scales, seg.e, N, K);
+    const int row[1] = {n0 + r < N ? n0 + r : -1};
+    for (int64_t p = 0; p < seg.count; p += kTile) {
+      const int rows = (int)(seg.count - p < kTile ? seg.count - p : kTile);
+      // rows beyond the group lie outside the descriptor
+      const __amdgpu_buffer_rsrc_t xb = buffer_of(x + (seg.begin + p) * K, (int64_t)rows * K * 2);
+      f32x4 acc[1] = {};
+      multiply<WT, 1>(m, row, xb, r < rows ? (uint32_t)r * (uint32_t)K * 2u : kOutside, steps * wave / waves,
+                      steps * (wave + 1) / waves, acc);
+      red_put<1>(red, wave, acc);
+      __syncthreads();
+      for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
+        const int c = i % kTile, q = i / kTile;
+        if (q < rows && n0 + c < N) {
+          const float v = red_sum<1>(red, waves, 0, q, c);
+          const int64_t at = (seg.begin + p + q) * (int64_t)N + n0 + c;
+          if constexpr (FP32) ((float *)y)[at] = v;
+          else ((uint16_t *)y)[at] = bf16_bits(v);
+        }
+      }
+      __syncthreads();
     }
   }
 }
@@ -444,159 +633,302 @@ __device__ __forceinline__ void find_expert(int j, const int32_t *__restrict__ t
   __syncthreads();
 }
 
-template <int WT, int RT, int MT>
-__device__ __forceinline__ void up_group(const Matrix &m, __amdgpu_buffer_rsrc_t x, int p0, int have,
-                                         const uint16_t *entry, int c0, int I, int K, FastDiv by_k,
-                                         uint16_t *h, float *red) {
-  constexpr int CT = RT / 2;  // channel tiles: CT of gate rows, CT of up rows
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  constexpr int waves = kThreads / kWave;
-  const int steps = (m.width + kStep - 1) / kStep;
-  int row[RT];
-  uint32_t tok[MT];
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int c = c0 + ct * kTile + (lane & 15);
-    row[ct] = c < I ? c : -1;
-    row[CT + ct] = c < I ? I + c : -1;
+// What the second launch reads: the number of active experts, and the j-th with its entries.
+__device__ __forceinline__ void note_expert(int j, int e, const FindLds &f, int32_t *active,
+                                            uint32_t *list, uint16_t *order) {
+  if (threadIdx.x == 0) {
+    if (j == 0) *active = f.active;
+    if (e >= 0) list[j] = (uint32_t)e | (uint32_t)f.before << 10 | (uint32_t)(f.have - 1) << 20;
   }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int p = p0 + mt * kTile + (lane & 15);
-    tok[mt] = p < have ? fast_div_apply(entry[p], by_k) * (uint32_t)m.width * 2u : kOutside;
-  }
-  f32x4 acc[MT][RT] = {};
-  multiply<WT, RT, MT, false>(m, row, x, tok, 0, steps * wave / waves, steps * (wave + 1) / waves,
-                              acc);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    red_put<RT>(red, wave, acc[mt]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTile * CT * kTile; i += kThreads) {
-      const int c = i % (CT * kTile), q = i / (CT * kTile), p = p0 + mt * kTile + q;
-      if (p < have && c0 + c < I) {
-        const float gate = red_sum<RT>(red, waves, c / kTile, q, c % kTile);
-        const float up = red_sum<RT>(red, waves, CT + c / kTile, q, c % kTile);
-        const float v = silu(gate) * up;
-        const uint16_t hi = bf16_bits(v);
-        const float rest = v - bf16_value(hi);
-        uint16_t *to = h + (int64_t)entry[p] * 2 * I + c0 + c;
-        to[0] = hi;
-        to[I] = (hi & 0x7F80) == 0x7F80 ? 0 : bf16_bits(rest);  // an infinity or NaN has no rest
-      }
-    }
-    __syncthreads();
-  }
+  if (e >= 0)
+    for (int i = threadIdx.x; i < f.have; i += kThreads) order[f.before + i] = f.entry[i];
 }
 
-template <int WT, int RT, int MTMAX>
-__global__ __launch_bounds__(kThreads) void ep_moe_up(
+// h of one entry and channel as a high and a low bf16 part.
+__device__ __forceinline__ void put_h(uint16_t *h, int entry, int I, int c, float gate, float up) {
+  const float v = silu(gate) * up;
+  const uint16_t hi = bf16_bits(v);
+  uint16_t *to = h + (int64_t)entry * 2 * I + c;
+  to[0] = hi;
+  to[I] = (hi & 0x7F80) == 0x7F80 ? 0 : bf16_bits(v - bf16_value(hi));  // an infinity or NaN has no rest
+}
+
+// Few units: a workgroup takes 16 channels of one expert, its four waves share the long axis.
+template <int WT>
+__global__ __launch_bounds__(kThreads) void ep_moe_up_split(
     const uint16_t *__restrict__ x, const int32_t *__restrict__ topk_idx,
     const void *__restrict__ w, const float *__restrict__ scales, int T, int H, int I, int K, int E,
     int64_t units, int tiles, FastDiv by_k, int32_t *__restrict__ active, uint32_t *__restrict__ list,
     uint16_t *__restrict__ order, uint16_t *__restrict__ h) {
+  constexpr int waves = kThreads / kWave;
   __shared__ FindLds f;
-  __shared__ float red[kThreads / kWave * RT * 4 * kWave];
+  __shared__ float red[waves * 2 * 4 * kWave];
+  const __amdgpu_buffer_rsrc_t xb = buffer_of(x, (int64_t)T * H * 2);
+  const int r = lane_id() & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int steps = (H + kStep - 1) / kStep;
+  int have_j = -1;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int j = (int)(u / tiles), tile = (int)(u - (int64_t)j * tiles);
+    if (j != have_j) find_expert(j, topk_idx, T * K, E, f);
+    have_j = j;
+    const int e = __builtin_amdgcn_readfirstlane(f.e), have = __builtin_amdgcn_readfirstlane(f.have);
+    if (tile == 0) note_expert(j, e, f, active, list, order);
+    if (e < 0) return;
+    const Matrix m = matrix_of<WT>(w, scales, e, 2 * (int64_t)I, H);
+    const int c0 = tile * kTile;
+    const int row[2] = {c0 + r < I ? c0 + r : -1, c0 + r < I ? I + c0 + r : -1};
+    for (int p0 = 0; p0 < have; p0 += kTile) {
+      f32x4 acc[2] = {};
+      multiply<WT, 2>(m, row, xb,
+                      p0 + r < have ? fast_div_apply(f.entry[p0 + r], by_k) * (uint32_t)H * 2u : kOutside,
+                      steps * wave / waves, steps * (wave + 1) / waves, acc);
+      red_put<2>(red, wave, acc);
+      __syncthreads();
+      const int c = threadIdx.x % kTile, q = threadIdx.x / kTile;
+      if (p0 + q < have && c0 + c < I)
+        put_h(h, f.entry[p0 + q], I, c0 + c, red_sum<2>(red, waves, 0, q, c), red_sum<2>(red, waves, 1, q, c));
+      __syncthreads();
+    }
+  }
+}
+
+template <int WT, int MT>
+__device__ __forceinline__ void up_wide_group(const Matrix &m, __amdgpu_buffer_rsrc_t x, int p0, int have,
+                                              const uint16_t *entry, int c0, int I, FastDiv by_k,
+                                              uint16_t *h, char *lds, uint32_t *tok_off) {
+  const int lane = lane_id(), g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (threadIdx.x < MT * kTile) {
+    const int p = p0 + (int)threadIdx.x;
+    tok_off[threadIdx.x] = p < have ? fast_div_apply(entry[p], by_k) * (uint32_t)m.width * 2u : kOutside;
+  }
+  __syncthreads();
+  constexpr int RT = kWideTiles, CT = RT / 2;
+  int row[RT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = c0 + (wave * CT + ct) * kTile + (lane & 15);
+    row[ct] = c < I ? c : -1;
+    row[CT + ct] = c < I ? I + c : -1;
+  }
+  f32x4 acc[MT][RT] = {};
+  multiply_wide<WT, RT, MT>(m, row, x, tok_off, lds, acc);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = p0 + mt * kTile + g * 4 + i;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+        if (p < have && row[ct] >= 0) put_h(h, entry[p], I, row[ct], acc[mt][ct][i], acc[mt][CT + ct][i]);
+    }
+}
+
+// Many units: a workgroup takes 64 channels (their gate and up rows) of one expert.
+template <int WT>
+__global__ __launch_bounds__(kThreads, 2) void ep_moe_up_wide(
+    const uint16_t *__restrict__ x, const int32_t *__restrict__ topk_idx,
+    const void *__restrict__ w, const float *__restrict__ scales, int T, int H, int I, int K, int E,
+    int64_t units, int tiles, FastDiv by_k, int32_t *__restrict__ active, uint32_t *__restrict__ list,
+    uint16_t *__restrict__ order, uint16_t *__restrict__ h) {
+  __shared__ __attribute__((aligned(16))) char lds[wide_lds_bytes<WT, 2>()];
+  __shared__ uint32_t tok_off[2 * kTile];
+  __shared__ FindLds f;
   const __amdgpu_buffer_rsrc_t xb = buffer_of(x, (int64_t)T * H * 2);
   int have_j = -1;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int j = (int)(u / tiles), tile = (int)(u - (int64_t)j * tiles);
     if (j != have_j) find_expert(j, topk_idx, T * K, E, f);
     have_j = j;
-    const int e = __builtin_amdgcn_readfirstlane(f.e), have = f.have;
-    if (tile == 0) {
-      if (threadIdx.x == 0) {
-        if (j == 0) *active = f.active;
-        if (e >= 0) list[j] = (uint32_t)e | (uint32_t)f.before << 10 | (uint32_t)(have - 1) << 20;
-      }
-      if (e >= 0)
-        for (int i = threadIdx.x; i < have; i += kThreads) order[f.before + i] = f.entry[i];
-    }
+    const int e = __builtin_amdgcn_readfirstlane(f.e), have = __builtin_amdgcn_readfirstlane(f.have);
+    if (tile == 0) note_expert(j, e, f, active, list, order);
     if (e < 0) return;
     const Matrix m = matrix_of<WT>(w, scales, e, 2 * (int64_t)I, H);
-    const int c0 = tile * (RT / 2) * kTile;
-    for (int p = 0; p < have;) {
-      const int left = have - p;
-      if (MTMAX > 2 && left > 2 * kTile) {
-        up_group<WT, RT, MTMAX>(m, xb, p, have, f.entry, c0, I, K, by_k, h, red);
-        p += MTMAX * kTile;
-      } else if (MTMAX > 1 && left > kTile) {
-        up_group<WT, RT, MTMAX < 2 ? 1 : 2>(m, xb, p, have, f.entry, c0, I, K, by_k, h, red);
-        p += 2 * kTile;
-      } else {
-        up_group<WT, RT, 1>(m, xb, p, have, f.entry, c0, I, K, by_k, h, red);
-        p += kTile;
-      }
+    for (int p = 0; p < have; p += 2 * kTile) {
+      if (have - p > kTile) up_wide_group<WT, 2>(m, xb, p, have, f.entry, tile * kWideTiles / 2 * 4 * kTile, I, by_k, h, lds, tok_off);
+      else up_wide_group<WT, 1>(m, xb, p, have, f.entry, tile * kWideTiles / 2 * 4 * kTile, I, by_k, h, lds, tok_off);
     }
+    __syncthreads();  // f is rewritten for the next unit
   }
 }
 
-template <int WT, int RT, int MT>
-__device__ __forceinline__ void down_group(const Matrix &m, __amdgpu_buffer_rsrc_t h, int p0, int have,
-                                           const uint16_t *order, int n0, int rows, int I, int s0,
-                                           int s1, float *part) {
-  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  int row[RT];
-  uint32_t tok[MT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) row[rt] = rt * kTile + r < rows ? n0 + rt * kTile + r : -1;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int p = p0 + mt * kTile + r;
-    tok[mt] = p < have ? (uint32_t)order[p] * (uint32_t)I * 4u : kOutside;
-  }
-  f32x4 acc[MT][RT] = {};
-  multiply<WT, RT, MT, true>(m, row, h, tok, (uint32_t)I * 2u, s0, s1, acc);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = p0 + mt * kTile + g * 4 + i;
-      if (p < have)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) part[(int)order[p] * (RT * kTile) + rt * kTile + r] = acc[mt][rt][i];
-    }
-}
+// Tokens go in groups of eight: rows 0 to 7 of the matrix instruction are their
+// high parts, rows 8 to 15 their low parts, so one instruction and one load per
+// lane serve both. An expert with more entries has its rows read again, from
+// the L2 that this wave has just filled. NG groups share a pass over the rows.
+// A wave's chunks form one stream over all its units, one chunk ahead.
+constexpr int kDownWaves = 8;
 
-template <int WT, int RT, int MTMAX>
-__global__ __launch_bounds__(1024) void ep_moe_down(
+template <int WT, int RT, int NG>
+__global__ __launch_bounds__(kDownWaves * kWave) void ep_moe_down(
     const uint16_t *__restrict__ h, const int32_t *__restrict__ topk_idx,
     const float *__restrict__ topk_weights, const uint16_t *__restrict__ bias,
     const void *__restrict__ w, const float *__restrict__ scales, int T, int H, int I, int K, int E,
     int rows, int tiles, int most_parts, const int32_t *__restrict__ active,
     const uint32_t *__restrict__ list, const uint16_t *__restrict__ order,
     uint16_t *__restrict__ out) {
+  using W = Weights<WT>;
+  constexpr int kChunkBytes = NG == 1 ? 256 : 128;  // of a weight row
+  constexpr int U = kChunkBytes / W::kStepBytes > 0 ? kChunkBytes / W::kStepBytes : 1;
+  constexpr int kTokens = 8 * NG;
   extern __shared__ float part[];  // [parts][n][RT * 16]
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
-  const int n = T * K;
-  const int steps = (I + kStep - 1) / kStep;
+  __shared__ uint32_t experts_lds[EP_MOE_MAX_ENTRIES];
+  __shared__ uint16_t order_lds[EP_MOE_MAX_ENTRIES];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int n = T * K, steps = (I + kStep - 1) / kStep, groups = I / kStep;
   const int experts = __builtin_amdgcn_readfirstlane(*active);
+  for (int i = threadIdx.x; i < n; i += kDownWaves * kWave) {
+    experts_lds[i] = list[i];
+    order_lds[i] = order[i];
+  }
+  __syncthreads();
   // parts of the long axis: enough units for every wave
-  int parts = experts > 0 ? (waves + experts - 1) / experts : 1;
+  int parts = experts > 0 ? (kDownWaves + experts - 1) / experts : 1;
   parts = parts < most_parts ? parts : most_parts;
+  const int units = experts * parts;
   const __amdgpu_buffer_rsrc_t hb = buffer_of(h, (int64_t)n * I * 4);
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int n0 = tile * rows, here = H - n0 < rows ? H - n0 : rows;
-    for (int u = wave; u < experts * parts; u += waves) {
-      const int j = u / parts, q = u - j * parts;
-      const MoeEntry a{(uint32_t)__builtin_amdgcn_readfirstlane((int)list[j])};
-      const Matrix m = matrix_of<WT>(w, scales, a.e(), H, I);
-      const uint16_t *mine = order + a.begin();
-      const int s0 = steps * q / parts, s1 = steps * (q + 1) / parts, have = a.count();
-      float *to = part + (int64_t)q * n * (RT * kTile);
-      for (int p = 0; p < have;) {
-        const int left = have - p;
-        if (MTMAX > 1 && left > kTile) {
-          down_group<WT, RT, MTMAX>(m, hb, p, have, mine, n0, here, I, s0, s1, to);
-          p += MTMAX * kTile;
-        } else {
-          down_group<WT, RT, 1>(m, hb, p, have, mine, n0, here, I, s0, s1, to);
-          p += kTile;
-        }
+
+  struct Place {  // of a chunk in the stream: unit, first entry of the group, step
+    int u, p, s, e, begin, have, s0, s1;
+  };
+  const auto enter = [&](Place &a) {  // the unit a.u
+    if (a.u >= units) return;
+    const int j = a.u / parts, q = a.u - j * parts;
+    const MoeEntry m{(uint32_t)__builtin_amdgcn_readfirstlane((int)experts_lds[j])};
+    a.e = m.e(), a.begin = m.begin(), a.have = m.count(), a.p = 0;
+    a.s = a.s0 = steps * q / parts, a.s1 = steps * (q + 1) / parts;
+  };
+  const auto next = [&](const Place &now) {
+    Place a = now;
+    a.s += U;
+    if (a.s >= a.s1) {
+      a.s = a.s0;
+      a.p += kTokens;
+      if (a.p >= a.have) {
+        a.u += kDownWaves;
+        enter(a);
       }
     }
+    return a;
+  };
+
+  struct Chunk {
+    u32x4 w[U][RT][W::kLoads], t[U][NG][4];
+    float scale[RT];
+  };
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int n0 = tile * rows, here = H - n0 < rows ? H - n0 : rows;
+    uint32_t wrow[RT], srow[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int at = rt * kTile + r;
+      wrow[rt] = at < here ? (uint32_t)(((int64_t)(n0 + at) * I * W::kStepBytes) / kStep) : kOutside;
+      srow[rt] = at < here ? (uint32_t)(n0 + at) * (uint32_t)groups * 4u : kOutside;
+    }
+    f32x4 acc[NG][RT];
+    const auto load = [&](Chunk &c, const Place &a) {
+      const Matrix m = matrix_of<WT>(w, scales, a.e, H, I);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int l = 0; l < W::kLoads; ++l)
+            c.w[u][rt][l] = load16(m.w, weight_at<WT>(I, wrow[rt], a.s + u, a.s1, l, g));
+      if constexpr (W::kScaled) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          c.scale[rt] = load4(m.scales, g < U && a.s + g < a.s1 ? srow[rt] + (uint32_t)(a.s + g) * 4u : kOutside);
+      }
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) {
+        const int p = a.p + ng * 8 + (r & 7);
+        const uint32_t tok = p < a.have ? ((uint32_t)order_lds[a.begin + p] * 2u + (r >> 3)) * (uint32_t)I * 2u : kOutside;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int s = a.s + u, k = s * kStep + W::place(j, g);
+            uint32_t off = s < a.s1 ? tok + (uint32_t)k * 2u : kOutside;
+            if constexpr (!W::kScaled) off = k < I ? off : kOutside;
+            c.t[u][ng][j] = load16(hb, off);
+          }
+      }
+    };
+    const auto add = [&](const Chunk &c, const Place &a) {
+      if (a.s == a.s0)
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) acc[ng][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u > 0 && a.s + u >= a.s1) break;
+        f32x4 sum[NG][RT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const bf16x8 b = W::operand(c.w[u][rt], j);
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+              const bf16x8 t = __builtin_bit_cast(bf16x8, c.t[u][ng][j]);
+              if constexpr (W::kScaled)
+                sum[ng][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    t, b, j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[ng][rt], 0, 0, 0);
+              else
+                acc[ng][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t, b, acc[ng][rt], 0, 0, 0);
+            }
+          }
+        if constexpr (W::kScaled) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const float sc = lane_value(c.scale[rt], u * 16 + r);
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[ng][rt][i] += sc * sum[ng][rt][i];
+          }
+        }
+      }
+      if (a.s + U < a.s1) return;
+      // the group's end: high and low parts are 32 lanes apart
+      float *const to = part + (int64_t)(a.u % parts) * n * (RT * kTile);
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = a.p + ng * 8 + (g & 1) * 4 + i;
+          const bool in = g < 2 && p < a.have;
+          const int entry = in ? order_lds[a.begin + p] : 0;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const float v = acc[ng][rt][i], both = v + lane_value(v, lane ^ 32);
+            if (in) to[entry * (RT * kTile) + rt * kTile + r] = both;
+          }
+        }
+    };
+    Place a, b;
+    a.u = wave;
+    enter(a);
+    Chunk ca, cb;
+    if (a.u < units) load(ca, a);
+    while (a.u < units) {
+      b = next(a);
+      if (b.u < units) load(cb, b);
+      __builtin_amdgcn_sched_barrier(0);
+      add(ca, a);
+      __builtin_amdgcn_sched_barrier(0);
+      if (b.u >= units) break;
+      a = next(b);
+      if (a.u < units) load(ca, a);
+      __builtin_amdgcn_sched_barrier(0);
+      add(cb, b);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < T * here; i += blockDim.x) {
+    for (int i = threadIdx.x; i < T * here; i += kDownWaves * kWave) {
       const int t = i / here, c = i - t * here;
       float sum = 0.f;
       for (int k = 0; k < K; ++k) {
@@ -616,34 +948,52 @@ __global__ __launch_bounds__(1024) void ep_moe_down(
 
 constexpr int kComputeUnits = 256;
 
-template <int WT, int RT>
-int matvec_launch(const ExpertMatvecArgs &a, int cap) {
-  const int tiles = (a.N + RT * kTile - 1) / (RT * kTile);
+template <int WT>
+int matvec_split_launch(const ExpertMatvecArgs &a, int cap) {
+  const int tiles = (a.N + kTile - 1) / kTile;
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
   const int64_t units = experts * tiles;
   const int steps = (a.K + kStep - 1) / kStep;
-  // few tiles: up to 16 waves share one tile's long axis
-  const int waves = units >= 2 * kComputeUnits || steps <= 4 ? 4 : (steps <= 8 ? 8 : 16);
+  const int waves = steps <= 4 ? 4 : (steps <= 8 ? 8 : 16);
   const int64_t most = cap > 0 ? cap : INT32_MAX;
   const unsigned blocks = (unsigned)(units < most ? units : most);
-  const size_t lds = (size_t)waves * RT * 4 * kWave * sizeof(float);
+  const size_t lds = (size_t)waves * 4 * kWave * sizeof(float);
   if (a.fp32)
-    ep_expert_matvec_tiles<WT, RT, true><<<blocks, waves * kWave, lds, a.stream>>>(
+    ep_expert_matvec_split<WT, true><<<blocks, waves * kWave, lds, a.stream>>>(
         (const uint16_t *)a.x, a.w, a.scales, a.counts, a.offsets, a.E, a.capacity, a.K, a.N, units,
         tiles, a.y);
   else
-    ep_expert_matvec_tiles<WT, RT, false><<<blocks, waves * kWave, lds, a.stream>>>(
+    ep_expert_matvec_split<WT, false><<<blocks, waves * kWave, lds, a.stream>>>(
         (const uint16_t *)a.x, a.w, a.scales, a.counts, a.offsets, a.E, a.capacity, a.K, a.N, units,
         tiles, a.y);
   return launch_status();
 }
 
-template <int WT, int WIDE>
+template <int WT>
+int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
+  constexpr int kRows = kWideTiles * 4 * kTile;
+  const int tiles = (a.N + kRows - 1) / kRows;
+  const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
+  const int64_t units = experts * tiles;
+  const int64_t most = cap > 0 ? cap : INT32_MAX;
+  const unsigned blocks = (unsigned)(units < most ? units : most);
+  if (a.fp32)
+    ep_expert_matvec_wide<WT, true><<<blocks, kThreads, 0, a.stream>>>(
+        (const uint16_t *)a.x, a.w, a.scales, a.counts, a.offsets, a.E, a.capacity, a.K, a.N, units,
+        tiles, a.y);
+  else
+    ep_expert_matvec_wide<WT, false><<<blocks, kThreads, 0, a.stream>>>(
+        (const uint16_t *)a.x, a.w, a.scales, a.counts, a.offsets, a.E, a.capacity, a.K, a.N, units,
+        tiles, a.y);
+  return launch_status();
+}
+
+template <int WT>
 int matvec_pick(const ExpertMatvecArgs &a, int cap) {
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
-  const int64_t wide_tiles = (a.N + WIDE * kTile - 1) / (WIDE * kTile);
-  return experts * wide_tiles >= 4 * kComputeUnits ? matvec_launch<WT, WIDE>(a, cap)
-                                                   : matvec_launch<WT, 1>(a, cap);
+  const int64_t wide_tiles = (a.N + 4 * kWideTiles * kTile - 1) / (4 * kWideTiles * kTile);
+  return experts * wide_tiles >= kComputeUnits ? matvec_wide_launch<WT>(a, cap)
+                                               : matvec_split_launch<WT>(a, cap);
 }
 
 struct MoeWorkspace {
@@ -653,57 +1003,64 @@ struct MoeWorkspace {
 };
 size_t moe_head_bytes(int64_t n) { return (size_t)((256 + 6 * n + 255) / 256 * 256); }
 
-template <int WT, int RT, int MTMAX>
-int moe_up_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
+template <int WT>
+int moe_up_split_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   const int n = a.T * a.K;
-  const int tiles = (a.I + RT / 2 * kTile - 1) / (RT / 2 * kTile);
+  const int tiles = (a.I + kTile - 1) / kTile;
   const int64_t units = (int64_t)(n < a.E ? n : a.E) * tiles;
   const unsigned blocks = (unsigned)(cap > 0 && units > cap ? cap : units);
-  ep_moe_up<WT, RT, MTMAX><<<blocks, kThreads, 0, a.stream>>>(
+  ep_moe_up_split<WT><<<blocks, kThreads, 0, a.stream>>>(
       (const uint16_t *)a.x, a.topk_idx, a.w_in, a.in_scales, a.T, a.H, a.I, a.K, a.E, units, tiles,
       fast_div((uint32_t)a.K), ws.active, ws.list, ws.order, ws.h);
   return launch_status();
 }
 
-template <int WT, int RT, int MTMAX>
+template <int WT>
+int moe_up_wide_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
+  const int n = a.T * a.K;
+  constexpr int kChannels = kWideTiles / 2 * 4 * kTile;
+  const int tiles = (a.I + kChannels - 1) / kChannels;
+  const int64_t units = (int64_t)(n < a.E ? n : a.E) * tiles;
+  const unsigned blocks = (unsigned)(cap > 0 && units > cap ? cap : units);
+  ep_moe_up_wide<WT><<<blocks, kThreads, 0, a.stream>>>(
+      (const uint16_t *)a.x, a.topk_idx, a.w_in, a.in_scales, a.T, a.H, a.I, a.K, a.E, units, tiles,
+      fast_div((uint32_t)a.K), ws.active, ws.list, ws.order, ws.h);
+  return launch_status();
+}
+
+template <int WT, int RT, int NG>
 int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int rows) {
   const int n = a.T * a.K;
   const int tiles = (a.H + rows - 1) / rows;
   constexpr int kLdsEntries = 1024;  // parts * entries kept in LDS: 64 or 128 KB
   const int steps = (a.I + kStep - 1) / kStep;
-  const int waves = 16;
   int parts = kLdsEntries / n;
-  parts = parts < waves ? parts : waves;
+  parts = parts < kDownWaves ? parts : kDownWaves;
   parts = parts < steps ? parts : steps;
   const unsigned blocks = (unsigned)(cap > 0 && tiles > cap ? cap : tiles);
   const size_t lds = (size_t)parts * n * RT * kTile * sizeof(float);
-  ep_moe_down<WT, RT, MTMAX><<<blocks, waves * kWave, lds, a.stream>>>(
+  ep_moe_down<WT, RT, NG><<<blocks, kDownWaves * kWave, lds, a.stream>>>(
       ws.h, a.topk_idx, a.topk_weights, (const uint16_t *)a.bias, a.w_out, a.out_scales, a.T, a.H, a.I,
       a.K, a.E, rows, tiles, parts, ws.active, ws.list, ws.order, (uint16_t *)a.out);
   return launch_status();
 }
 
-template <int WT, int WIDE>
+template <int WT>
 int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
-  const bool few = a.T * a.K <= kTile;  // no expert can have a second token tile
-  int rc;
-  if (WIDE == 2) {
-    rc = few ? moe_up_launch<WT, 2, 1>(a, ws, cap) : moe_up_launch<WT, 2, 4>(a, ws, cap);
-  } else {
-    const int n = a.T * a.K;
-    const int64_t wide_units = (int64_t)(n < a.E ? n : a.E) * ((a.I + 31) / 32);
-    const bool wide = wide_units >= 4 * kComputeUnits;
-    if (wide) rc = few ? moe_up_launch<WT, WIDE, 1>(a, ws, cap) : moe_up_launch<WT, WIDE, 4>(a, ws, cap);
-    else rc = few ? moe_up_launch<WT, 2, 1>(a, ws, cap) : moe_up_launch<WT, 2, 4>(a, ws, cap);
-  }
+  const int n = a.T * a.K;
+  constexpr int kChannels = kWideTiles / 2 * 4 * kTile;
+  const int64_t wide_units = (int64_t)(n < a.E ? n : a.E) * ((a.I + kChannels - 1) / kChannels);
+  const int rc = wide_units >= kComputeUnits ? moe_up_wide_launch<WT>(a, ws, cap)
+                                             : moe_up_split_launch<WT>(a, ws, cap);
   if (rc != 0) return rc;
   // Output rows per workgroup: an even share of the chip's 256 compute units, at most two tiles.
   int rows = (a.H + kComputeUnits - 1) / kComputeUnits;
   rows = (rows + 3) / 4 * 4;
   rows = rows < 2 * kTile ? rows : 2 * kTile;
+  const bool many = n > 8 * a.E;  // entries per expert, on the average
   if (rows <= kTile)
-    return few ? moe_down_launch<WT, 1, 1>(a, ws, cap, rows) : moe_down_launch<WT, 1, 2>(a, ws, cap, rows);
-  return few ? moe_down_launch<WT, 2, 1>(a, ws, cap, rows) : moe_down_launch<WT, 2, 2>(a, ws, cap, rows);
+    return many ? moe_down_launch<WT, 1, 2>(a, ws, cap, rows) : moe_down_launch<WT, 1, 1>(a, ws, cap, rows);
+  return many ? moe_down_launch<WT, 2, 2>(a, ws, cap, rows) : moe_down_launch<WT, 2, 1>(a, ws, cap, rows);
 }
 
 }  // namespace
@@ -711,9 +1068,9 @@ int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
 int launch_expert_matvec(const ExpertMatvecArgs &a) {
   if (a.capacity == 0) return 0;
   const int cap = stream_workgroup_limit(a.stream);
-  if (a.dtype == EP_BF16) return matvec_pick<EP_BF16, 2>(a, cap);
-  if (a.dtype == EP_FP8_E4M3) return matvec_pick<EP_FP8_E4M3, 2>(a, cap);
-  return matvec_pick<EP_FP4X2, 4>(a, cap);
+  if (a.dtype == EP_BF16) return matvec_pick<EP_BF16>(a, cap);
+  if (a.dtype == EP_FP8_E4M3) return matvec_pick<EP_FP8_E4M3>(a, cap);
+  return matvec_pick<EP_FP4X2>(a, cap);
 }
 
 size_t moe_layer_workspace(int T, int K, int I) {
@@ -728,9 +1085,9 @@ int launch_moe_layer(const MoeLayerArgs &a) {
   char *p = (char *)a.workspace;
   MoeWorkspace ws{(int32_t *)p, (uint32_t *)(p + 256), (uint16_t *)(p + 256 + 4 * (size_t)n),
                   (uint16_t *)(p + moe_head_bytes(n))};
-  if (a.dtype == EP_BF16) return moe_pick<EP_BF16, 2>(a, ws, cap);
-  if (a.dtype == EP_FP8_E4M3) return moe_pick<EP_FP8_E4M3, 2>(a, ws, cap);
-  return moe_pick<EP_FP4X2, 4>(a, ws, cap);
+  if (a.dtype == EP_BF16) return moe_pick<EP_BF16>(a, ws, cap);
+  if (a.dtype == EP_FP8_E4M3) return moe_pick<EP_FP8_E4M3>(a, ws, cap);
+  return moe_pick<EP_FP4X2>(a, ws, cap);
 }
 
 }  // namespace ep
