@@ -34,6 +34,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 constexpr int kLane = 8;      // channels per lane
 constexpr int kMaxRows = 32;  // rows per block: bits of the mask
+constexpr int kCodePolicy = 2 | 16;  // nt, sc1
 
 // 1 / (1 + exp(-z)). EXACT (binary32 rows) uses the accurate exponential and
 // division; bf16 rows the hardware's exp2 and reciprocal, whose error (about
@@ -44,13 +45,20 @@ __device__ __forceinline__ float sigmoid(float z) {
   else return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
+// Stores are non-temporal, those of 16-byte pieces that fill whole lines at
+// device scope as well (95 against 104 us forward, 126 against 138 backward at
+// prefill). Binary32 rows leave every second 16 bytes of a line to a second
+// store, which device scope would send to memory in halves (50 against 15 us
+// at 3000 rows of 1408): not there. Loads are plain (nt: 116 against 110 us).
 template <bool FP32>
 struct Row {  // eight consecutive values of a row of bf16 or binary32
-  static constexpr int kBytes = kLane * (FP32 ? 4 : 2);
+  static constexpr int kElt = FP32 ? 4 : 2;
+  static constexpr int kPolicy = FP32 ? 2 : 2 | 16;  // nt, sc1
+
   static __device__ __forceinline__ void load(const char *p, float (&v)[kLane]) {
-    const u32x4 a = __builtin_nontemporal_load((const u32x4 *)p);
+    const u32x4 a = *(const u32x4 *)p;
     if constexpr (FP32) {
-      const u32x4 b = __builtin_nontemporal_load((const u32x4 *)p + 1);
+      const u32x4 b = *((const u32x4 *)p + 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
     } else {
@@ -61,23 +69,30 @@ struct Row {  // eight consecutive values of a row of bf16 or binary32
       }
     }
   }
-  static __device__ __forceinline__ void store(char *p, const float (&v)[kLane]) {
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t to, uint32_t off,
+                                               const float (&v)[kLane]) {
     u32x4 a, b;
     if constexpr (FP32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(v[i]), b[i] = __float_as_uint(v[4 + i]);
-      __builtin_nontemporal_store(a, (u32x4 *)p);
-      __builtin_nontemporal_store(b, (u32x4 *)p + 1);
+      __builtin_amdgcn_raw_buffer_store_b128(b, to, (int)off + 16, 0, kPolicy);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f32x2 f = {v[2 * i], v[2 * i + 1]};
         a[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
       }
-      __builtin_nontemporal_store(a, (u32x4 *)p);
     }
+    __builtin_amdgcn_raw_buffer_store_b128(a, to, (int)off, 0, kPolicy);
   }
 };
+
+// Rows [r0, r0 + n) of an array of rows of `bytes` bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void *p, int64_t r0, int n, int64_t bytes) {
+  constexpr int kRawBufferFlags = 0x00020000;
+  return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(p) + r0 * bytes, (short)0,
+                                           (int)(n * bytes), kRawBufferFlags);
+}
 
 __device__ __forceinline__ float row_max(float v) {  // over the 16 lanes of a row
   constexpr int kRowRor = 0x120;
@@ -157,13 +172,15 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
     int64_t blocks, FastDiv by_chunks, char *__restrict__ h, char *__restrict__ codes,
     float *__restrict__ scales) {
   __shared__ uint32_t lds;
-  constexpr int kElt = FP32 ? 4 : 2;
+  constexpr int kElt = Row<FP32>::kElt;
   const int chunks = I / kLane;
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t r0 = b * block_rows;
     const int n = (int)(capacity - r0 < block_rows ? capacity - r0 : block_rows);
     const uint32_t real = real_rows(counts, offsets, E, r0, n, &lds);
     if (real == 0) continue;
+    const __amdgpu_buffer_rsrc_t to_h = rows_of(h, r0, n, (int64_t)I * kElt);
+    const __amdgpu_buffer_rsrc_t to_codes = SAVE ? rows_of(codes, r0, n, 2 * (int64_t)I) : to_h;
     for (uint32_t c = threadIdx.x; c < (uint32_t)(n * chunks); c += kThreads) {
       const uint32_t r = fast_div_apply(c, by_chunks), i = (c - r * (uint32_t)chunks) * kLane;
       if (!(real >> r & 1)) continue;
@@ -173,13 +190,12 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
       Row<FP32>::load(gate_up + (row * 2 * I + I + i) * kElt, u);
 #pragma unroll
       for (int q = 0; q < kLane; ++q) v[q] = g[q] * sigmoid<FP32>(g[q]) * u[q];
-      Row<FP32>::store(h + (row * I + i) * kElt, v);
+      Row<FP32>::store(to_h, (r * I + i) * kElt, v);
       if constexpr (SAVE) {
         float sg, su;
         const u32x2 cg = quantize(g, sg), cu = quantize(u, su);
-        char *to = codes + row * 2 * I + i;
-        __builtin_nontemporal_store(cg, (u32x2 *)to);
-        __builtin_nontemporal_store(cu, (u32x2 *)(to + I));
+        __builtin_amdgcn_raw_buffer_store_b64(cg, to_codes, (int)(r * 2 * I + i), 0, kCodePolicy);
+        __builtin_amdgcn_raw_buffer_store_b64(cu, to_codes, (int)(r * 2 * I + I + i), 0, kCodePolicy);
         if ((threadIdx.x & 15) == 0) {
           float *st = scales + row * (2 * I / 128) + i / 128;
           st[0] = sg;
@@ -197,20 +213,22 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_backward_rows(
     int I, int block_rows, int64_t blocks, FastDiv by_chunks, char *__restrict__ d_gate_up,
     char *__restrict__ h) {
   __shared__ uint32_t lds;
-  constexpr int kElt = FP32 ? 4 : 2;
+  constexpr int kElt = Row<FP32>::kElt;
   const int chunks = I / kLane;
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t r0 = b * block_rows;
     const int n = (int)(capacity - r0 < block_rows ? capacity - r0 : block_rows);
     const uint32_t real = real_rows(counts, offsets, E, r0, n, &lds);
     if (real == 0) continue;
+    const __amdgpu_buffer_rsrc_t to_d = rows_of(d_gate_up, r0, n, 2 * (int64_t)I * kElt);
+    const __amdgpu_buffer_rsrc_t to_h = WITH_H ? rows_of(h, r0, n, (int64_t)I * kElt) : to_d;
     for (uint32_t c = threadIdx.x; c < (uint32_t)(n * chunks); c += kThreads) {
       const uint32_t r = fast_div_apply(c, by_chunks), i = (c - r * (uint32_t)chunks) * kLane;
       if (!(real >> r & 1)) continue;
       const int64_t row = r0 + r;
       const char *from = codes + row * 2 * I + i;
-      const u32x2 cg = __builtin_nontemporal_load((const u32x2 *)from);
-      const u32x2 cu = __builtin_nontemporal_load((const u32x2 *)(from + I));
+      const u32x2 cg = *(const u32x2 *)from;
+      const u32x2 cu = *(const u32x2 *)(from + I);
       const float *sc = scales + row * (2 * I / 128) + i / 128;
       float d[kLane], g[kLane], u[kLane], dg[kLane], du[kLane], v[kLane];
       Row<FP32>::load(dh + (row * I + i) * kElt, d);
@@ -223,9 +241,9 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_backward_rows(
         du[q] = d[q] * gs;
         if constexpr (WITH_H) v[q] = gs * u[q];
       }
-      Row<FP32>::store(d_gate_up + (row * 2 * I + i) * kElt, dg);
-      Row<FP32>::store(d_gate_up + (row * 2 * I + I + i) * kElt, du);
-      if constexpr (WITH_H) Row<FP32>::store(h + (row * I + i) * kElt, v);
+      Row<FP32>::store(to_d, (r * 2 * I + i) * kElt, dg);
+      Row<FP32>::store(to_d, (r * 2 * I + I + i) * kElt, du);
+      if constexpr (WITH_H) Row<FP32>::store(to_h, (r * I + i) * kElt, v);
     }
   }
 }
@@ -235,11 +253,15 @@ struct RowGrid {
   int64_t blocks;
   unsigned launch;
 };
-// Rows per block: enough to spread the search for the real ones over several
-// rows, as long as there are still eight workgroups for every compute unit.
-RowGrid row_grid(int64_t capacity, int cap) {
-  int64_t rows = capacity / 2048;
-  rows = rows < 1 ? 1 : (rows < 16 ? rows : 16);
+// Rows per block: about two chunks of eight channels for every thread, and an
+// odd number, which spreads the blocks that run together over the memory's
+// channels (at prefill, rows of 8 KB: 3 rows 88 us forward and 119 backward, 2
+// rows 95 and 126, 8 rows 101 and 134), as long as there are still eight
+// workgroups for every compute unit.
+RowGrid row_grid(int64_t capacity, int chunks, int cap) {
+  int64_t rows = 2 * kThreads / chunks | 1;
+  if (rows > capacity / 2048) rows = capacity / 2048;
+  rows = rows < 1 ? 1 : (rows < kMaxRows ? rows : kMaxRows);
   const int64_t blocks = (capacity + rows - 1) / rows;
   const int64_t most = cap > 0 ? cap : (1 << 22);
   return {(int)rows, blocks, (unsigned)(blocks < most ? blocks : most)};
@@ -249,7 +271,7 @@ RowGrid row_grid(int64_t capacity, int cap) {
 
 int launch_swiglu(const SwigluArgs &a) {
   if (a.capacity == 0) return 0;
-  const RowGrid g = row_grid(a.capacity, stream_workgroup_limit(a.stream));
+  const RowGrid g = row_grid(a.capacity, a.I / kLane, stream_workgroup_limit(a.stream));
   const FastDiv by = fast_div((uint32_t)(a.I / kLane));
   const auto run = [&](auto kernel) {
     kernel<<<g.launch, kThreads, 0, a.stream>>>((const char *)a.gate_up, a.counts, a.offsets, a.E,
@@ -263,7 +285,7 @@ int launch_swiglu(const SwigluArgs &a) {
 
 int launch_swiglu_backward(const SwigluBackwardArgs &a) {
   if (a.capacity == 0) return 0;
-  const RowGrid g = row_grid(a.capacity, stream_workgroup_limit(a.stream));
+  const RowGrid g = row_grid(a.capacity, a.I / kLane, stream_workgroup_limit(a.stream));
   const FastDiv by = fast_div((uint32_t)(a.I / kLane));
   const auto run = [&](auto kernel) {
     kernel<<<g.launch, kThreads, 0, a.stream>>>(
