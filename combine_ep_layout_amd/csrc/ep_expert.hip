@@ -390,44 +390,41 @@ __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float
 // ------------------------------------------------------------ ep_expert_matvec
 
 // The j-th expert that has rows, found by every wave for itself from the
-// counts (a ballot for every 64 experts); absent: e = -1. A count is cut to
-// the rows that lie inside the buffer, so no access leaves it whatever the
-// arrays hold.
+// counts (a ballot for every 64 experts); absent: e = -1. A span is cut to the
+// rows that lie inside the buffer, so no access leaves it whatever the arrays
+// hold.
 struct Segment {
   int e;
   int64_t begin, count;
 };
-__device__ __forceinline__ int64_t rows_inside(const int32_t *counts, const int32_t *offsets, int e,
-                                               int64_t capacity) {
-  const int64_t b = offsets[e], c = counts[e];
-  return b < 0 || b >= capacity ? 0 : (c < capacity - b ? c : capacity - b);
-}
 __device__ __forceinline__ Segment find_segment(int j, const int32_t *__restrict__ counts,
                                                 const int32_t *__restrict__ offsets, int E,
                                                 int64_t capacity) {
   if (counts == nullptr) return {j == 0 ? 0 : -1, 0, capacity};
   const int lane = lane_id();
-  int e = -1;
-  for (int first = 0; first < E && e < 0; first += 4 * kWave) {
-    uint64_t have[4];
+  Segment s{-1, 0, 0};
+  for (int first = 0; first < E && s.e < 0; first += 4 * kWave) {
+    int begin[4], count[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int at = first + q * kWave + lane;
-      have[q] = ballot(at < E && rows_inside(counts, offsets, at, capacity) > 0);
+      const int e = first + q * kWave + lane;
+      begin[q] = e < E ? offsets[e] : -1;
+      count[q] = e < E ? counts[e] : 0;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int n = __builtin_popcountll(have[q]);
-      if (e < 0 && j < n) {
-        const uint64_t hit = ballot((have[q] >> lane & 1) != 0 && count_below(have[q]) == j);
-        e = first + q * kWave + __builtin_ctzll(hit);
+      if (begin[q] < 0 || begin[q] >= capacity) count[q] = 0;
+      else if (count[q] > capacity - begin[q]) count[q] = (int)(capacity - begin[q]);
+      const uint64_t have = ballot(count[q] > 0);
+      const int n = __builtin_popcountll(have);
+      if (s.e < 0 && j < n) {
+        const int at = __builtin_ctzll(ballot((have >> lane & 1) != 0 && count_below(have) == j));
+        s = {first + q * kWave + at, read_lane(begin[q], at), read_lane(count[q], at)};
       }
       j -= n;
     }
   }
-  if (e < 0) return {-1, 0, 0};
-  return {e, __builtin_amdgcn_readfirstlane(offsets[e]),
-          __builtin_amdgcn_readfirstlane((int)rows_inside(counts, offsets, e, capacity))};
+  return s;
 }
 
 template <int WT, int MT, bool FP32>
@@ -757,10 +754,13 @@ __global__ __launch_bounds__(kThreads, 2) void ep_moe_up_wide(
 // lane serve both. An expert with more entries has its rows read again, from
 // the L2 that this wave has just filled. NG groups share a pass over the rows.
 // A wave's chunks form one stream over all its units, one chunk ahead.
-constexpr int kDownWaves = 8;
+// Waves per workgroup: 8 of up to 256 registers each; with one row tile and
+// half the chunk a wave needs half as many, and 16 waves are faster (45 tokens,
+// hidden 336: 18 against 21 us).
+constexpr int down_waves(int row_tiles, int groups) { return row_tiles == 1 && groups == 1 ? 16 : 8; }
 
 template <int WT, int RT, int NG>
-__global__ __launch_bounds__(kDownWaves * kWave) void ep_moe_down(
+__global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
     const uint16_t *__restrict__ h, const int32_t *__restrict__ topk_idx,
     const float *__restrict__ topk_weights, const uint16_t *__restrict__ bias,
     const void *__restrict__ w, const float *__restrict__ scales, int T, int H, int I, int K, int E,
@@ -768,7 +768,8 @@ __global__ __launch_bounds__(kDownWaves * kWave) void ep_moe_down(
     const uint32_t *__restrict__ list, const uint16_t *__restrict__ order,
     uint16_t *__restrict__ out) {
   using W = Weights<WT>;
-  constexpr int kChunkBytes = NG == 1 ? 256 : 128;  // of a weight row
+  constexpr int kDownWaves = down_waves(RT, NG);
+  constexpr int kChunkBytes = NG == 1 ? (RT == 1 ? 128 : 256) : 128;  // of a weight row
   constexpr int U = kChunkBytes / W::kStepBytes > 0 ? kChunkBytes / W::kStepBytes : 1;
   constexpr int kTokens = 8 * NG;
   extern __shared__ float part[];  // [parts][n][RT * 16]
@@ -783,8 +784,9 @@ __global__ __launch_bounds__(kDownWaves * kWave) void ep_moe_down(
     order_lds[i] = order[i];
   }
   __syncthreads();
-  // parts of the long axis: enough units for every wave
-  int parts = experts > 0 ? (kDownWaves + experts - 1) / experts : 1;
+  // parts of the long axis: two units for every wave, so that an uneven number of experts does
+  // not leave half of the waves without work (one token: 123 against 131 us with one)
+  int parts = experts > 0 ? (2 * kDownWaves + experts - 1) / experts : 1;
   parts = parts < most_parts ? parts : most_parts;
   const int units = experts * parts;
   const __amdgpu_buffer_rsrc_t hb = buffer_of(h, (int64_t)n * I * 4);
@@ -947,6 +949,7 @@ __global__ __launch_bounds__(kDownWaves * kWave) void ep_moe_down(
 }
 
 constexpr int kComputeUnits = 256;
+constexpr int64_t kMaxBlocks = (1 << 22) - 1;  // of at most 1024 threads: within the grid limit of 2^32
 
 template <int WT>
 int matvec_split_launch(const ExpertMatvecArgs &a, int cap) {
@@ -955,7 +958,7 @@ int matvec_split_launch(const ExpertMatvecArgs &a, int cap) {
   const int64_t units = experts * tiles;
   const int steps = (a.K + kStep - 1) / kStep;
   const int waves = steps <= 4 ? 4 : (steps <= 8 ? 8 : 16);
-  const int64_t most = cap > 0 ? cap : INT32_MAX;
+  const int64_t most = cap > 0 ? cap : kMaxBlocks;
   const unsigned blocks = (unsigned)(units < most ? units : most);
   const size_t lds = (size_t)waves * 4 * kWave * sizeof(float);
   if (a.fp32)
@@ -975,7 +978,7 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
   const int tiles = (a.N + kRows - 1) / kRows;
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
   const int64_t units = experts * tiles;
-  const int64_t most = cap > 0 ? cap : INT32_MAX;
+  const int64_t most = cap > 0 ? cap : kMaxBlocks;
   const unsigned blocks = (unsigned)(units < most ? units : most);
   if (a.fp32)
     ep_expert_matvec_wide<WT, true><<<blocks, kThreads, 0, a.stream>>>(
@@ -992,8 +995,9 @@ template <int WT>
 int matvec_pick(const ExpertMatvecArgs &a, int cap) {
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
   const int64_t wide_tiles = (a.N + 4 * kWideTiles * kTile - 1) / (4 * kWideTiles * kTile);
-  return experts * wide_tiles >= kComputeUnits ? matvec_wide_launch<WT>(a, cap)
-                                               : matvec_split_launch<WT>(a, cap);
+  const int64_t units = experts * wide_tiles;
+  const bool wide = units >= kComputeUnits || (units >= kComputeUnits / 4 && a.capacity > 32 * experts);
+  return wide ? matvec_wide_launch<WT>(a, cap) : matvec_split_launch<WT>(a, cap);
 }
 
 struct MoeWorkspace {
@@ -1008,7 +1012,8 @@ int moe_up_split_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) 
   const int n = a.T * a.K;
   const int tiles = (a.I + kTile - 1) / kTile;
   const int64_t units = (int64_t)(n < a.E ? n : a.E) * tiles;
-  const unsigned blocks = (unsigned)(cap > 0 && units > cap ? cap : units);
+  const int64_t most = cap > 0 ? cap : kMaxBlocks;
+  const unsigned blocks = (unsigned)(units < most ? units : most);
   ep_moe_up_split<WT><<<blocks, kThreads, 0, a.stream>>>(
       (const uint16_t *)a.x, a.topk_idx, a.w_in, a.in_scales, a.T, a.H, a.I, a.K, a.E, units, tiles,
       fast_div((uint32_t)a.K), ws.active, ws.list, ws.order, ws.h);
@@ -1021,7 +1026,8 @@ int moe_up_wide_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   constexpr int kChannels = kWideTiles / 2 * 4 * kTile;
   const int tiles = (a.I + kChannels - 1) / kChannels;
   const int64_t units = (int64_t)(n < a.E ? n : a.E) * tiles;
-  const unsigned blocks = (unsigned)(cap > 0 && units > cap ? cap : units);
+  const int64_t most = cap > 0 ? cap : kMaxBlocks;
+  const unsigned blocks = (unsigned)(units < most ? units : most);
   ep_moe_up_wide<WT><<<blocks, kThreads, 0, a.stream>>>(
       (const uint16_t *)a.x, a.topk_idx, a.w_in, a.in_scales, a.T, a.H, a.I, a.K, a.E, units, tiles,
       fast_div((uint32_t)a.K), ws.active, ws.list, ws.order, ws.h);
@@ -1034,8 +1040,9 @@ int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int 
   const int tiles = (a.H + rows - 1) / rows;
   constexpr int kLdsEntries = 1024;  // parts * entries kept in LDS: 64 or 128 KB
   const int steps = (a.I + kStep - 1) / kStep;
+  constexpr int kDownWaves = down_waves(RT, NG);
   int parts = kLdsEntries / n;
-  parts = parts < kDownWaves ? parts : kDownWaves;
+  parts = parts < 2 * kDownWaves ? parts : 2 * kDownWaves;
   parts = parts < steps ? parts : steps;
   const unsigned blocks = (unsigned)(cap > 0 && tiles > cap ? cap : tiles);
   const size_t lds = (size_t)parts * n * RT * kTile * sizeof(float);

@@ -82,6 +82,21 @@ MATVEC = [
 ]
 
 
+# Enough tiles for the kernels that take 128 rows of a matrix at once: 40 experts x 8 tiles.
+WIDE_COUNTS = [1, 0, 16, 17, 32, 33, 70, 2] * 5
+MATVEC += [
+    ("bf16", 1160, 904, WIDE_COUNTS, 8, "fp32"),
+    ("bf16", 128, 1024, WIDE_COUNTS, 1, "bf16"),
+    ("bf16", 24, 1000, WIDE_COUNTS, 1, "fp32"),
+    ("fp8", 128, 904, WIDE_COUNTS, 1, "fp32"),
+    ("fp8", 640, 912, WIDE_COUNTS, 16, "bf16"),
+    ("fp4", 128, 904, WIDE_COUNTS, 1, "fp32"),
+    ("fp4", 640, 904, WIDE_COUNTS, 4, "fp32"),
+    ("fp4", 1024, 2056, WIDE_COUNTS, 1, "bf16"),
+    ("bf16", 512, 1024, [100] * 9, 1, "bf16"),  # 72 tiles, many rows each
+]
+
+
 @pytest.mark.parametrize("kind,K,N,counts,A,out", MATVEC)
 def test_matvec(kind, K, N, counts, A, out):
     _say(f"[matvec] {kind} K={K} N={N} counts={counts} A={A} {out}")
@@ -211,6 +226,13 @@ LAYER = [
     (33, 8, 40, 2048, 384, "fp4", 0.1, False, True, False),
     (128, 8, 64, 7168, 512, "fp4", 0.0, False, True, True),
     (128, 8, 4, 256, 128, "fp4", 0.0, True, True, False),  # 250 entries per expert
+    # enough units for the kernels that take 64 channels at once
+    (24, 4, 64, 1160, 264, "bf16", 0.1, True, True, True),
+    (100, 8, 40, 136, 456, "bf16", 0.0, False, True, False),  # 20 entries per expert
+    (60, 8, 48, 384, 384, "fp8", 0.2, False, True, True),
+    (120, 8, 20, 128, 896, "fp8", 0.0, False, False, False),  # 48 entries per expert
+    (40, 4, 64, 640, 256, "fp4", 0.1, True, True, False),
+    (4, 2, 64, 4096, 2048, "fp4", 0.0, False, True, False),  # 8 entries, 32 tiles each
 ]
 
 
@@ -482,6 +504,17 @@ def test_wgrad_scales_that_are_no_powers_of_two():
     _check_wgrad(a)
 
 
+def test_wgrad_scales_of_every_kind_side_by_side():
+    """Powers of two inside and outside the range that converts directly, zeros, negative scales,
+    subnormal ones and ordinary ones, in rows of one step."""
+    a = _wgrad_case("fp8", 256, 136, [40, 70], 1, "fp32", False, True)
+    kinds = torch.tensor([1.0, 2.0 ** -70, 0.0, -2.0, 0.75, 2.0 ** 66, -0.0, 2.0 ** -130, 2.0 ** 64, 2.0 ** -64], device=DEV)
+    a["s"][:] = kinds[torch.arange(a["s"].numel(), device=DEV) % 10].view_as(a["s"])
+    _run_wgrad(a)
+    torch.cuda.synchronize()
+    _check_wgrad(a)
+
+
 @pytest.mark.parametrize("grad", ["bf16", "fp32"])
 def test_wgrad_accumulates_in_place(grad):
     a = _wgrad_case("bf16", 264, 136, [40, 0, 3], 1, grad, True, False)
@@ -521,7 +554,17 @@ def _cases_of_all():
     keep = codes.clone(), scales.clone()
     B.ep_swiglu(v, c, o, 4, cap, I, B.EP_BF16, h, *keep)
     torch.cuda.synchronize()
+    wide = _layer_case(24, 4, 64, 392, 264, "bf16", 0.1)
+    full = _layer_case(128, 8, 64, 7168, 128, "fp4")  # 1024 entries: the most LDS of the second launch
+    many = [9, 0, 40, 17] * 10
+    mc, mo, _, mcap = _spans(many, 1)
+    mw, ms = _weights(40, 904, 384, "fp8", gen)
+    mx = _normal((mcap, 384), gen, 1.0, torch.bfloat16)
+    my = torch.zeros(mcap, 904, dtype=torch.bfloat16, device=DEV)
     return [
+        ("wide layer", lambda st: _run_layer(wide, stream=st), [wide["out"]]),
+        ("full layer", lambda st: _run_layer(full, stream=st), [full["out"]]),
+        ("wide matvec", lambda st: B.ep_expert_matvec(mx, mw, ms, mc, mo, 40, mcap, 384, 904, B.EP_FP8_E4M3, my, B.EP_BF16, st), [my]),
         ("layer", lambda st: _run_layer(lay, stream=st), [lay["out"]]),
         ("matvec", lambda st: B.ep_expert_matvec(x, w, s, c, o, 4, cap, 384, 200, B.EP_FP4X2, y, B.EP_FP32, st), [y]),
         ("swiglu", lambda st: B.ep_swiglu(v, c, o, 4, cap, I, B.EP_BF16, h, codes, scales, st), [h, codes, scales]),
@@ -574,6 +617,19 @@ def test_captured_calls_replay_with_the_eager_results():
             call(None)  # the program's own eager call between replays
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, _bits(outs))), name
+
+
+def test_one_workspace_serves_calls_in_order():
+    """A larger call leaves its lists behind; a smaller one on the same stream must not see them."""
+    a, b = _layer_case(100, 8, 64, 256, 128, "bf16", seed=3), _layer_case(3, 2, 64, 256, 128, "bf16", seed=4)
+    b["idx"][1] = -1
+    b["ws"] = a["ws"]
+    for _ in range(3):
+        _run_layer(a)
+        _run_layer(b)
+    torch.cuda.synchronize()
+    _check_layer(a)
+    _check_layer(b)
 
 
 def test_two_streams_at_once_with_their_own_workspaces():
@@ -673,3 +729,65 @@ def test_training_chain_on_eight_bit_rows():
     common = dict(c=counts, o=offsets, rows=rows, cap=cap, prev=None, E=E, grad="fp32")
     _check_wgrad(dict(common, dy=dZ, x=X, s=Xs, dw=dWin, N=2 * I, H=H, kind="fp8"))
     _check_wgrad(dict(common, dy=dY, x=H2, s=None, dw=dWout, N=H, H=I, kind="bf16"))
+
+
+def test_rows_and_matrices_behind_four_gib():
+    """Rows at the end of buffers of more than 2^32 bytes, and the last expert's matrix of more
+    than 2^32 bytes of them: every offset that passes 32 bits is taken in 64."""
+    gen = _gen(14)
+    cap, K, N, n = 300_000, 8192, 256, 5
+    c = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    o = torch.tensor([0, cap - n, cap], dtype=torch.int32, device=DEV)
+    x = torch.empty(cap, K, dtype=torch.bfloat16, device=DEV)
+    x[-n:] = _normal((n, K), gen, 1.0, torch.bfloat16)
+    w, _ = _weights(2, N, K, "bf16", gen)
+    y = torch.empty(cap, N, device=DEV)
+    B.ep_expert_matvec(x, w, None, c, o, 2, cap, K, N, B.EP_BF16, y, B.EP_FP32)
+    h = torch.empty(cap, K // 2, dtype=torch.bfloat16, device=DEV)
+    codes = torch.empty(cap, K, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(cap, K // 128, device=DEV)
+    B.ep_swiglu(x, c, o, 2, cap, K // 2, B.EP_BF16, h, codes, scales)
+    d = torch.empty_like(x)
+    B.ep_swiglu_backward(h, codes, scales, c, o, 2, cap, K // 2, B.EP_BF16, d)
+    dw = torch.empty(2, N, K, device=DEV)
+    dy = torch.empty(cap, N, dtype=torch.bfloat16, device=DEV)
+    dy[-n:] = _normal((n, N), gen, 1.0, torch.bfloat16)
+    B.ep_expert_wgrad(dy, x, None, c, o, 2, cap, N, K, B.EP_BF16, None, dw, B.EP_FP32)
+    torch.cuda.synchronize()
+    z = x[-n:].double()
+    want, err = R.product(z, torch.zeros_like(z), w[1].double())
+    R.near(y[-n:], want, err, torch.float32)
+    half = K // 2
+    zero = torch.zeros_like(z[:, :half])
+    want, err = R.gated(z[:, :half], zero, z[:, half:], zero)
+    R.near(h[-n:], want, err, torch.bfloat16)
+    code, scale = R.checkpoint(x[-n:])
+    assert torch.equal(scales[-n:].double(), scale)
+    assert torch.equal(codes[-n:].view(torch.float8_e4m3fn).double(), code)
+    v = R.values(codes[-n:], scales[-n:], "fp8")
+    want, err = R.gated_backward(h[-n:].double(), v[:, :half], v[:, half:])
+    R.near(d[-n:], want, err, torch.bfloat16)
+    a = dy[-n:].double()
+    assert bool((dw[0] == 0).all())
+    R.near(dw[1], a.T @ z, (n + 9) * R.U * (a.abs().T @ z.abs()), torch.float32)
+    del x, y, h, codes, d, dw, dy
+    # the gradient and the weights of 40 experts: 4.7 GB each
+    E, N, H, n = 40, 4096, 7168, 3
+    counts = [0] * (E - 1) + [n]
+    c, o, _, cap = _spans(counts, 1)
+    x = _normal((cap, H), gen, 1.0, torch.bfloat16)
+    dy = _normal((cap, N), gen, 1.0, torch.bfloat16)
+    dw = torch.full((E, N, H), NAN, device=DEV)
+    B.ep_expert_wgrad(dy, x, None, c, o, E, cap, N, H, B.EP_BF16, None, dw, B.EP_FP32)
+    w = torch.empty(2 * E, N, H, dtype=torch.bfloat16, device=DEV)
+    w[-1] = _normal((N, H), gen, H ** -0.5, torch.bfloat16)
+    y = torch.empty(cap, N, device=DEV)
+    B.ep_expert_matvec(x, w, None, torch.cat([torch.zeros(E, dtype=torch.int32, device=DEV), c]),
+                       torch.cat([torch.zeros(E, dtype=torch.int32, device=DEV), o]), 2 * E, cap, H, N, B.EP_BF16, y,
+                       B.EP_FP32)
+    torch.cuda.synchronize()
+    a, z = dy.double(), x.double()
+    R.near(dw[-1], a.T @ z, (n + 9) * R.U * (a.abs().T @ z.abs()), torch.float32)
+    assert bool((dw[:-1] == 0).all())
+    want, err = R.product(z, torch.zeros_like(z), w[-1].double())
+    R.near(y, want, err, torch.float32)
