@@ -8,14 +8,24 @@
 // of a row; then a group's 128 products are summed first and the sum is
 // scaled (the codes are exact in bf16, so no weight is ever rounded).
 //
-// What bounds it: with at most a few tokens per expert every weight is used
-// a few times, so the time is that of reading the active experts' weights
-// from HBM once. The products run on the matrix cores (16x16x32 bf16) all the
-// same: a wave takes 16 weight rows per tile as one operand, straight from
-// memory into registers (each row's 64 consecutive bytes go to four lanes:
-// nothing is shared between waves, so LDS would only add a trip), and 16
-// tokens as the other; lanes of absent tokens and rows are given an offset
-// outside the buffer descriptor, which reads as 0 and costs no traffic.
+// What bounds it: with a few tokens per expert every weight is used a few
+// times, so the time is that of reading the active experts' weights from HBM
+// once. The products run on the matrix cores (16x16x32 bf16) all the same: a
+// wave takes 16 weight rows per tile as one operand, straight from memory into
+// registers (each row's 64 consecutive bytes go to four lanes; nothing is
+// shared between waves, so LDS would only add a trip), and 16 tokens as the
+// other; lanes of absent tokens and rows are given an offset outside the
+// buffer descriptor, which reads as 0 and costs no traffic. What carries it:
+// loads a whole chunk ahead of the products and held there (the compiler,
+// left alone, moves them down to their use: 503 against 355 us for a decode
+// batch's fp4 products), 256 consecutive bytes of a row per chunk (64: 351
+// against 255 us), the tokens' values through LDS once for four waves, and
+// plain loads (non-temporal ones lose 5 to 30%: 53 against 41 us in the second
+// launch of one token).
+// Measured on MI355X: a bf16 layer of one token, top-8, hidden 7168,
+// intermediate 2048 (705 MB of weights) 123 us, 5.7 TB/s; 128 tokens over 197
+// active fp4 experts of 256 (4.6 GB) 1277 us, 3.6 TB/s; fp4 products of 1024
+// rows over 64 experts, 7168 to 4096 (1.0 GB) 226 us, 4.5 TB/s.
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -534,15 +544,18 @@ __global__ __launch_bounds__(1024) void ep_expert_matvec_split(
 // ---------------------------------------------------------------- ep_moe_layer
 //
 // First launch: workgroup (j, tile) finds the j-th expert that occurs in
-// topk_idx and its entries by itself (n = T*K <= 1024 ids, no extra launch),
-// its four waves split the long axis of 16 or 32 channels' gate and up rows,
-// and h goes to the workspace as a high and a low bf16 part per value, so
-// that the second product loses nothing to the rounding of h. The workgroups
-// of tile 0 leave the list of active experts and their entries behind.
-// Second launch: a workgroup owns up to 32 output channels of every token;
-// its waves take (expert, part of the long axis) units, the entries' results
-// stay in LDS, and are summed with their router weights in k order, so the
-// result is a pure function of the inputs.
+// topk_idx and its entries by itself (n = T*K <= 1024 ids, no extra launch)
+// and computes gate, up and h for 16 or 64 channels; h goes to the workspace
+// as a high and a low bf16 part per value (2^-17 relative), so that the second
+// product loses nothing to the rounding of h. The workgroups of tile 0 leave
+// the list of active experts and their entries behind.
+// Second launch: a workgroup owns up to 32 output channels of every token (an
+// even share for 256 compute units: 28 of 7168); its waves take (expert, part
+// of the long axis) units, the entries' results stay in LDS, and are summed
+// with their router weights in k order, so the result is a pure function of
+// the inputs. What bounds it beyond a few dozen entries is h, which every
+// workgroup reads whole: 595 us for 1024 entries over 197 fp4 experts, 371
+// with the loads of h left out.
 
 struct MoeEntry {  // one active expert, packed: id, first place in the order, entries - 1
   uint32_t v;
@@ -741,9 +754,10 @@ __global__ __launch_bounds__(kThreads, 2) void ep_moe_up_wide(
     if (tile == 0) note_expert(j, e, f, active, list, order);
     if (e < 0) return;
     const Matrix m = matrix_of<WT>(w, scales, e, 2 * (int64_t)I, H);
+    const int c0 = tile * (kWideTiles / 2 * 4 * kTile);
     for (int p = 0; p < have; p += 2 * kTile) {
-      if (have - p > kTile) up_wide_group<WT, 2>(m, xb, p, have, f.entry, tile * kWideTiles / 2 * 4 * kTile, I, by_k, h, lds, tok_off);
-      else up_wide_group<WT, 1>(m, xb, p, have, f.entry, tile * kWideTiles / 2 * 4 * kTile, I, by_k, h, lds, tok_off);
+      if (have - p > kTile) up_wide_group<WT, 2>(m, xb, p, have, f.entry, c0, I, by_k, h, lds, tok_off);
+      else up_wide_group<WT, 1>(m, xb, p, have, f.entry, c0, I, by_k, h, lds, tok_off);
     }
     __syncthreads();  // f is rewritten for the next unit
   }
@@ -991,6 +1005,13 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
   return launch_status();
 }
 
+// The wide kernel reads x once for 128 rows and walks the whole long axis: right
+// where its workgroups fill the chip (256 of them), or come near it and the
+// split kernel would read every matrix again for each 16 of many rows: 16
+// experts of 64 rows, 2048 to 1024 in bf16 (128 workgroups), 51 against 92 us.
+// Else waves that share the long axis are faster: one row of an fp4 matrix 7168
+// to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 40 against 70,
+// 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 12 against 15.
 template <int WT>
 int matvec_pick(const ExpertMatvecArgs &a, int cap) {
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
@@ -1052,6 +1073,13 @@ int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int 
   return launch_status();
 }
 
+// First launch: 64 channels a workgroup where these fill the chip (28 fp8
+// entries of 20 experts, hidden 2048, 240 to 336 workgroups: 15 against 20 us;
+// 8 bf16 experts of one token, 256 workgroups: 80 us either way), else 16 and
+// the long axis shared (one bf16 expert, 32 workgroups: 18 against 54 us).
+// Second launch: two groups of eight tokens a pass where experts have more than
+// eight entries on the average (64 fp4 experts, 16 entries each: 393 against
+// 434 us), else one (197 active experts, 5 entries each: 619 against 655).
 template <int WT>
 int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   const int n = a.T * a.K;
@@ -1064,7 +1092,7 @@ int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   int rows = (a.H + kComputeUnits - 1) / kComputeUnits;
   rows = (rows + 3) / 4 * 4;
   rows = rows < 2 * kTile ? rows : 2 * kTile;
-  const bool many = n > 8 * a.E;  // entries per expert, on the average
+  const bool many = n > 8 * a.E;
   if (rows <= kTile)
     return many ? moe_down_launch<WT, 1, 2>(a, ws, cap, rows) : moe_down_launch<WT, 1, 1>(a, ws, cap, rows);
   return many ? moe_down_launch<WT, 2, 2>(a, ws, cap, rows) : moe_down_launch<WT, 2, 1>(a, ws, cap, rows);

@@ -478,8 +478,9 @@ int ep_moe_layer(const void *x, const int32_t *topk_idx, const float *topk_weigh
 /*
  * Per-expert matrix-vector products for a few rows per expert:
  *   y[r] = w[e] x[r]  for the rows r of each expert e
- * summed in binary32, rounded once. Any number of rows is right; beyond
- * about 64 per expert the weights are read again for every 64.
+ * summed in binary32, rounded once. Any number of rows is right; beyond 32
+ * per expert (16 for a few small matrices) the weights are read again for
+ * every 32, from cache where they fit.
  *
  *   x             bf16 [capacity_rows, in_features], an expand buffer
  *   w             [num_experts, out_features, in_features] of weight_dtype
@@ -519,7 +520,8 @@ int ep_swiglu(const void *gate_up, const int32_t *counts, const int32_t *offsets
  * scale, s = 1 / (1 + exp(-gate)), for the experts' rows
  *   d_gate_up = [dh * up * s * (1 + gate * (1 - s)) | dh * gate * s]
  *   h         = gate * s * up   (unless h is NULL: for the next weight gradient)
- * in binary32, rounded once. Any finite fp32 scales are accepted.
+ * in binary32, rounded once. Any finite fp32 scales are accepted. With bf16
+ * rows, s is taken as 0 where it is below 2^-126 (gate under -87).
  *
  *   dh          [capacity_rows, intermediate] of dtype (EP_BF16, EP_FP32)
  *   d_gate_up   [capacity_rows, 2 * intermediate] of dtype
