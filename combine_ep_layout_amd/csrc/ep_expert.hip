@@ -11,9 +11,8 @@
 // What bounds it: with a few tokens per expert every weight is used a few
 // times, so the time is that of reading the active experts' weights from HBM
 // once. The products run on the matrix cores (16x16x32 bf16) all the same: a
-// wave takes 16 weight rows per tile as one operand, straight from memory into
-// registers (each row's 64 consecutive bytes go to four lanes; nothing is
-// shared between waves, so LDS would only add a trip), and 16 tokens as the
+// wave takes 16 weight rows per tile as one operand, from memory into registers
+// (each row's 64 consecutive bytes go to four lanes), and 16 tokens as the
 // other; lanes of absent tokens and rows are given an offset outside the
 // buffer descriptor, which reads as 0 and costs no traffic. What carries it:
 // loads a whole chunk ahead of the products and held there (the compiler,
@@ -24,8 +23,8 @@
 // launch of one token).
 // Measured on MI355X: a bf16 layer of one token, top-8, hidden 7168,
 // intermediate 2048 (705 MB of weights) 123 us, 5.7 TB/s; 128 tokens over 197
-// active fp4 experts of 256 (4.6 GB) 1277 us, 3.6 TB/s; fp4 products of 1024
-// rows over 64 experts, 7168 to 4096 (1.0 GB) 226 us, 4.5 TB/s.
+// active fp4 experts of 256 (4.6 GB) 1046 us, 4.4 TB/s; fp4 products of 1024
+// rows over 64 experts, 7168 to 4096 (1.0 GB) 207 us, 4.9 TB/s.
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -50,6 +49,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
                                            kRawBufferFlags);
 }
+// The offset where `in`, else one outside every descriptor; arithmetic, because a choice between
+// two offsets becomes a branch, and a value loaded in a branch is waited for at its end.
+__device__ __forceinline__ uint32_t only(bool in, uint32_t off) { return off | (uint32_t)!in << 31; }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0);
 }
@@ -155,7 +157,29 @@ template <int WT>
 __device__ __forceinline__ uint32_t weight_at(int width, uint32_t wrow, int s, int s1, int l, int g) {
   using W = Weights<WT>;
   const bool in = s < s1 && (W::kScaled || s * kStep + W::place(l, g) < width);
-  return in ? wrow + (uint32_t)s * W::kStepBytes + W::load_byte(l, g) : kOutside;
+  return only(in, wrow + (uint32_t)s * W::kStepBytes + W::load_byte(l, g));
+}
+
+// 64 consecutive bytes of 16 weight rows, loaded with the lanes as the matrix
+// instruction wants them, have neighbouring lanes in 16 different rows: 64
+// accesses, one a cycle, for 1 KB (the address units were busy for 81% of the
+// launches of a large layer). So four neighbouring lanes load a row's 64 bytes
+// (16 accesses) and the values change lanes through 1 KB of LDS of the wave's
+// own before their use: 16 bf16 experts of 64 rows, 2048 to 1024, 40 against 51
+// us; an fp4 layer's launches 640 and 500 against 680 and 595. The kernels that
+// split the long axis are bound by latency and load as the instruction wants
+// it. Lane l loads row l / 4 and the 16 bytes (l % 4) ^ (l / 16)
+// of it, so that the 16 lanes that read one piece of every row use all banks.
+__device__ __forceinline__ int near_row() { return lane_id() >> 2; }
+__device__ __forceinline__ int near_piece() { return (lane_id() & 3) ^ (lane_id() >> 4); }
+constexpr int kTurnBytes = kWave * 16;  // of LDS per wave
+__device__ __forceinline__ u32x4 turn(char *slot, const u32x4 &v) {
+  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  *(u32x4 *)(slot + lane * 16) = v;  // a wave's LDS accesses keep their order
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  const u32x4 got = *(const u32x4 *)(slot + (r * 4 + (g ^ (r >> 2))) * 16);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  return got;
 }
 
 // acc[rt] += rows x tokens over steps [s0, s1), a wave on its own. Lane
@@ -185,7 +209,7 @@ struct Chunk {  // kSteps steps' operands on their way into registers
     if constexpr (W::kScaled) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
-        scale[rt] = load4(m.scales, g < kSteps && s + g < s1 ? srow[rt] + (uint32_t)(s + g) * 4u : kOutside);
+        scale[rt] = load4(m.scales, only(g < kSteps && s + g < s1, srow[rt] + (uint32_t)(s + g) * 4u));
     }
 #pragma unroll
     for (int u = 0; u < kSteps; ++u)
@@ -193,7 +217,7 @@ struct Chunk {  // kSteps steps' operands on their way into registers
       for (int j = 0; j < 4; ++j) {
         const int k = (s + u) * kStep + W::place(j, g);
         const bool in = s + u < s1 && (W::kScaled || k < m.width);
-        t[u][j] = load16(x, in ? tok + (uint32_t)k * 2u : kOutside);
+        t[u][j] = load16(x, only(in, tok + (uint32_t)k * 2u));
       }
   }
 
@@ -266,7 +290,8 @@ __device__ __forceinline__ float red_sum(const float *red, int waves, int rt, in
 // The same product for a workgroup of four waves with different rows and the
 // same tokens, over the whole long axis: the tokens' values come through LDS,
 // loaded once for all four waves, a chunk of 256 bytes of every weight row
-// ahead of the products.
+// ahead of the products. near[rt] is the weight row that this lane loads
+// (near_row of the tile; negative: absent).
 template <int WT>
 struct WideChunk {
   using W = Weights<WT>;
@@ -276,11 +301,11 @@ struct WideChunk {
 };
 template <int WT, int MT>
 constexpr int wide_lds_bytes() {
-  return 2 * MT * kTile * WideChunk<WT>::kTokenBytes;
+  return 2 * MT * kTile * WideChunk<WT>::kTokenBytes + kThreads / kWave * kTurnBytes;
 }
 
 template <int WT, int RT, int MT>
-__device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[RT],
+__device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&near)[RT],
                                               __amdgpu_buffer_rsrc_t x, const uint32_t *tok_off,
                                               char *lds, f32x4 (&acc)[MT][RT]) {
   using W = Weights<WT>;
@@ -289,7 +314,9 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
   const int tid = threadIdx.x, lane = lane_id(), r = lane & 15, g = lane >> 4;
   const int steps = (m.width + kStep - 1) / kStep, chunks = (steps + C::kSteps - 1) / C::kSteps;
   uint32_t wrow[RT], srow[RT];
-  row_offsets<WT>(m, row, wrow, srow);
+  row_offsets<WT>(m, near, wrow, srow);
+  const int piece_of = near_piece(), step_of = lane & 3;
+  char *const slot = lds + 2 * MT * kTile * C::kTokenBytes + tid / kWave * kTurnBytes;
   // A token's pieces are rotated by its number (exclusive or), so that 16 tokens' pieces of the
   // same place, which 16 lanes read at once, lie in different banks.
   uint32_t from[kMine];
@@ -300,19 +327,19 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
     piece[i] = (at % C::kPieces) ^ (t & 15);
     from[i] = tok_off[t] + (uint32_t)piece[i] * 16u;
   }
-  u32x4 xs[kMine], w[2][C::kSteps][RT][W::kLoads];
+  u32x4 xs[kMine], xs0[kMine], w[2][C::kSteps][RT][W::kLoads];
   float scale[2][RT];
-  const auto load_x = [&](int c) {
+  const auto load_x = [&](u32x4 (&to)[kMine], int c) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const bool in = W::kScaled ? c < chunks : c * C::kValues + piece[i] * 8 < m.width;
-      xs[i] = load16(x, in ? from[i] + (uint32_t)c * C::kTokenBytes : kOutside);
+      to[i] = load16(x, only(in, from[i] + (uint32_t)c * C::kTokenBytes));
     }
   };
-  const auto store_x = [&](int c) {
+  const auto store_x = [&](const u32x4 (&v)[kMine], int c) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
-      *(u32x4 *)(lds + (c & 1) * (MT * kTile * C::kTokenBytes) + (tid + i * kThreads) * 16) = xs[i];
+      *(u32x4 *)(lds + (c & 1) * (MT * kTile * C::kTokenBytes) + (tid + i * kThreads) * 16) = v[i];
   };
   const auto load_w = [&](int c, auto set) {
 #pragma unroll
@@ -321,10 +348,10 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
       for (int u = 0; u < C::kSteps; ++u)
 #pragma unroll
         for (int l = 0; l < W::kLoads; ++l)
-          w[set][u][rt][l] = load16(m.w, weight_at<WT>(m.width, wrow[rt], c * C::kSteps + u, steps, l, g));
+          w[set][u][rt][l] = load16(m.w, weight_at<WT>(m.width, wrow[rt], c * C::kSteps + u, steps, l, piece_of));
       if constexpr (W::kScaled) {
-        const int s = c * C::kSteps + g;
-        scale[set][rt] = load4(m.scales, g < C::kSteps && s < steps ? srow[rt] + (uint32_t)s * 4u : kOutside);
+        const int s = c * C::kSteps + step_of;
+        scale[set][rt] = load4(m.scales, only(step_of < C::kSteps && s < steps, srow[rt] + (uint32_t)s * 4u));
       }
     }
   };
@@ -333,6 +360,11 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
 #pragma unroll
     for (int u = 0; u < C::kSteps; ++u) {
       if (u > 0 && c * C::kSteps + u >= steps) break;
+      u32x4 turned[RT][W::kLoads];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int l = 0; l < W::kLoads; ++l) turned[rt][l] = turn(slot, w[set][u][rt][l]);
       f32x4 part[MT][RT];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -343,7 +375,7 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
                                     (((u * kStep + W::place(j, g)) / 8) ^ r) * 16);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const bf16x8 b = W::operand(w[set][u][rt], j);
+          const bf16x8 b = W::operand(turned[rt], j);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             if constexpr (W::kScaled)
@@ -357,7 +389,7 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
       if constexpr (W::kScaled) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const float sc = lane_value(scale[set][rt], u * 16 + r);
+          const float sc = lane_value(scale[set][rt], r * 4 + u);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -368,25 +400,28 @@ __device__ __forceinline__ void multiply_wide(const Matrix &m, const int (&row)[
   };
   constexpr std::integral_constant<int, 0> even{};
   constexpr std::integral_constant<int, 1> odd{};
-  load_x(0);
+  // Loads come back in order, so the tokens' are always issued before the weights': the wait for
+  // them is then none for the weights of the next chunk (680 to 640 us with those mixed, 580 so).
+  const auto chunk = [&](int c, auto use, auto fill) {
+    store_x(xs, c + 1);
+    load_x(xs, c + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(c + 1, fill);
+    __builtin_amdgcn_sched_barrier(0);
+    add(c, use);
+    __syncthreads();
+  };
+  load_x(xs0, 0);
+  load_x(xs, 1);
+  __builtin_amdgcn_sched_barrier(0);
   load_w(0, even);
-  store_x(0);
-  load_x(1);
+  __builtin_amdgcn_sched_barrier(0);
+  store_x(xs0, 0);
   __syncthreads();
   for (int c = 0; c < chunks; c += 2) {
-    store_x(c + 1);
-    load_x(c + 2);
-    load_w(c + 1, odd);
-    __builtin_amdgcn_sched_barrier(0);
-    add(c, even);
-    __syncthreads();
+    chunk(c, even, odd);
     if (c + 1 >= chunks) break;
-    store_x(c + 2);
-    load_x(c + 3);
-    load_w(c + 2, even);
-    __builtin_amdgcn_sched_barrier(0);
-    add(c + 1, odd);
-    __syncthreads();
+    chunk(c + 1, odd, even);
   }
 }
 
@@ -448,14 +483,15 @@ __device__ __forceinline__ void matvec_wide_group(const Matrix &m, const uint16_
   if (threadIdx.x < MT * kTile)
     tok_off[threadIdx.x] = (int)threadIdx.x < rows ? threadIdx.x * (uint32_t)m.width * 2u : kOutside;
   __syncthreads();
-  int row[RT];
+  int row[RT], near[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    const int n = n0 + (wave * RT + rt) * kTile + r;
-    row[rt] = n < N ? n : -1;
+    const int first = n0 + (wave * RT + rt) * kTile;
+    row[rt] = first + r < N ? first + r : -1;
+    near[rt] = first + near_row() < N ? first + near_row() : -1;
   }
   f32x4 acc[MT][RT] = {};
-  multiply_wide<WT, RT, MT>(m, row, xb, tok_off, lds, acc);
+  multiply_wide<WT, RT, MT>(m, near, xb, tok_off, lds, acc);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -553,9 +589,9 @@ __global__ __launch_bounds__(1024) void ep_expert_matvec_split(
 // even share for 256 compute units: 28 of 7168); its waves take (expert, part
 // of the long axis) units, the entries' results stay in LDS, and are summed
 // with their router weights in k order, so the result is a pure function of
-// the inputs. What bounds it beyond a few dozen entries is h, which every
-// workgroup reads whole: 595 us for 1024 entries over 197 fp4 experts, 371
-// with the loads of h left out.
+// the inputs. Beyond a few dozen entries h weighs as much as the weights, since
+// every workgroup reads it whole: 465 us for 1024 entries over 197 fp4 experts
+// (1.5 GB of weights).
 
 struct MoeEntry {  // one active expert, packed: id, first place in the order, entries - 1
   uint32_t v;
@@ -568,11 +604,13 @@ struct FindLds {
   int count[EP_MAX_EXPERTS];
   uint16_t entry[EP_MOE_MAX_ENTRIES];
   int wave_active[4], wave_entries[4];
-  int e, before, have, active, next;
+  int same[EP_MOE_MAX_ENTRIES / kWave];  // entries of the expert in each 64 ids
+  int e, before, have, active;
 };
 
 // The j-th active expert (first occurrence order for n <= 64, ascending id
-// above): e or -1, its `have` entries in f.entry, `before` entries of other
+// above): e or -1, its `have` entries in f.entry in ascending order (every
+// workgroup of an expert has to place them alike), `before` entries of other
 // experts ahead of it in the order, and the number of active experts. 256
 // threads, ends synchronised.
 __device__ __forceinline__ void find_expert(int j, const int32_t *__restrict__ topk_idx, int n, int E,
@@ -602,7 +640,7 @@ __device__ __forceinline__ void find_expert(int j, const int32_t *__restrict__ t
     return;
   }
   for (int i = tid; i < EP_MAX_EXPERTS; i += kThreads) f.count[i] = 0;
-  if (tid == 0) f.e = -1, f.next = 0;
+  if (tid == 0) f.e = -1;
   __syncthreads();
   int id[EP_MOE_MAX_ENTRIES / kThreads];
 #pragma unroll
@@ -635,10 +673,20 @@ __device__ __forceinline__ void find_expert(int j, const int32_t *__restrict__ t
   if (tid == 0) f.active = total;
   __syncthreads();
   const int e = f.e;
-  if (e >= 0) {
+  constexpr int kIds = EP_MOE_MAX_ENTRIES / kThreads, kWaves = kThreads / kWave;
+  uint64_t same[kIds];
 #pragma unroll
-    for (int q = 0; q < EP_MOE_MAX_ENTRIES / kThreads; ++q)
-      if (id[q] == e) f.entry[atomicAdd(&f.next, 1)] = (uint16_t)(tid + q * kThreads);
+  for (int q = 0; q < kIds; ++q) {
+    same[q] = ballot(e >= 0 && id[q] == e);
+    if (lane == 0) f.same[q * kWaves + wave] = __builtin_popcountll(same[q]);
+  }
+  __syncthreads();
+  int first = 0;
+#pragma unroll
+  for (int i = 0; i < kIds * kWaves; ++i) {
+    if (i % kWaves == wave && (same[i / kWaves] >> lane & 1) != 0)
+      f.entry[first + count_below(same[i / kWaves])] = (uint16_t)(tid + i / kWaves * kThreads);
+    first += f.same[i];
   }
   __syncthreads();
 }
@@ -654,13 +702,16 @@ __device__ __forceinline__ void note_expert(int j, int e, const FindLds &f, int3
     for (int i = threadIdx.x; i < f.have; i += kThreads) order[f.before + i] = f.entry[i];
 }
 
-// h of one entry and channel as a high and a low bf16 part.
-__device__ __forceinline__ void put_h(uint16_t *h, int entry, int I, int c, float gate, float up) {
+// h of one entry and channel as a high and a low bf16 part. The workspace holds
+// [I / 8][n][high, low][8] values, the entries in the order of their experts: the
+// second launch's lanes, a part of an entry each, then read consecutive pieces of
+// 16 bytes.
+__device__ __forceinline__ void put_h(uint16_t *h, int n, int at, int c, float gate, float up) {
   const float v = silu(gate) * up;
   const uint16_t hi = bf16_bits(v);
-  uint16_t *to = h + (int64_t)entry * 2 * I + c;
+  uint16_t *to = h + ((int64_t)(c >> 3) * n + at) * 16 + (c & 7);
   to[0] = hi;
-  to[I] = (hi & 0x7F80) == 0x7F80 ? 0 : bf16_bits(v - bf16_value(hi));  // an infinity or NaN has no rest
+  to[8] = (hi & 0x7F80) == 0x7F80 ? 0 : bf16_bits(v - bf16_value(hi));  // an infinity or NaN has no rest
 }
 
 // Few units: a workgroup takes 16 channels of one expert, its four waves share the long axis.
@@ -682,6 +733,7 @@ __global__ __launch_bounds__(kThreads) void ep_moe_up_split(
     if (j != have_j) find_expert(j, topk_idx, T * K, E, f);
     have_j = j;
     const int e = __builtin_amdgcn_readfirstlane(f.e), have = __builtin_amdgcn_readfirstlane(f.have);
+    const int before = __builtin_amdgcn_readfirstlane(f.before);
     if (tile == 0) note_expert(j, e, f, active, list, order);
     if (e < 0) return;
     const Matrix m = matrix_of<WT>(w, scales, e, 2 * (int64_t)I, H);
@@ -696,7 +748,7 @@ __global__ __launch_bounds__(kThreads) void ep_moe_up_split(
       __syncthreads();
       const int c = threadIdx.x % kTile, q = threadIdx.x / kTile;
       if (p0 + q < have && c0 + c < I)
-        put_h(h, f.entry[p0 + q], I, c0 + c, red_sum<2>(red, waves, 0, q, c), red_sum<2>(red, waves, 1, q, c));
+        put_h(h, T * K, before + p0 + q, c0 + c, red_sum<2>(red, waves, 0, q, c), red_sum<2>(red, waves, 1, q, c));
       __syncthreads();
     }
   }
@@ -705,7 +757,7 @@ __global__ __launch_bounds__(kThreads) void ep_moe_up_split(
 template <int WT, int MT>
 __device__ __forceinline__ void up_wide_group(const Matrix &m, __amdgpu_buffer_rsrc_t x, int p0, int have,
                                               const uint16_t *entry, int c0, int I, FastDiv by_k,
-                                              uint16_t *h, char *lds, uint32_t *tok_off) {
+                                              int n, int before, uint16_t *h, char *lds, uint32_t *tok_off) {
   const int lane = lane_id(), g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (threadIdx.x < MT * kTile) {
@@ -714,15 +766,16 @@ __device__ __forceinline__ void up_wide_group(const Matrix &m, __amdgpu_buffer_r
   }
   __syncthreads();
   constexpr int RT = kWideTiles, CT = RT / 2;
-  int row[RT];
+  int row[CT], near[RT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    const int c = c0 + (wave * CT + ct) * kTile + (lane & 15);
+    const int first = c0 + (wave * CT + ct) * kTile, c = first + (lane & 15), from = first + near_row();
     row[ct] = c < I ? c : -1;
-    row[CT + ct] = c < I ? I + c : -1;
+    near[ct] = from < I ? from : -1;
+    near[CT + ct] = from < I ? I + from : -1;
   }
   f32x4 acc[MT][RT] = {};
-  multiply_wide<WT, RT, MT>(m, row, x, tok_off, lds, acc);
+  multiply_wide<WT, RT, MT>(m, near, x, tok_off, lds, acc);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -730,7 +783,7 @@ __device__ __forceinline__ void up_wide_group(const Matrix &m, __amdgpu_buffer_r
       const int p = p0 + mt * kTile + g * 4 + i;
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
-        if (p < have && row[ct] >= 0) put_h(h, entry[p], I, row[ct], acc[mt][ct][i], acc[mt][CT + ct][i]);
+        if (p < have && row[ct] >= 0) put_h(h, n, before + p, row[ct], acc[mt][ct][i], acc[mt][CT + ct][i]);
     }
 }
 
@@ -751,21 +804,22 @@ __global__ __launch_bounds__(kThreads, 2) void ep_moe_up_wide(
     if (j != have_j) find_expert(j, topk_idx, T * K, E, f);
     have_j = j;
     const int e = __builtin_amdgcn_readfirstlane(f.e), have = __builtin_amdgcn_readfirstlane(f.have);
+    const int before = __builtin_amdgcn_readfirstlane(f.before);
     if (tile == 0) note_expert(j, e, f, active, list, order);
     if (e < 0) return;
     const Matrix m = matrix_of<WT>(w, scales, e, 2 * (int64_t)I, H);
     const int c0 = tile * (kWideTiles / 2 * 4 * kTile);
     for (int p = 0; p < have; p += 2 * kTile) {
-      if (have - p > kTile) up_wide_group<WT, 2>(m, xb, p, have, f.entry, c0, I, by_k, h, lds, tok_off);
-      else up_wide_group<WT, 1>(m, xb, p, have, f.entry, c0, I, by_k, h, lds, tok_off);
+      if (have - p > kTile) up_wide_group<WT, 2>(m, xb, p, have, f.entry, c0, I, by_k, T * K, before, h, lds, tok_off);
+      else up_wide_group<WT, 1>(m, xb, p, have, f.entry, c0, I, by_k, T * K, before, h, lds, tok_off);
     }
     __syncthreads();  // f is rewritten for the next unit
   }
 }
 
-// Tokens go in groups of eight: rows 0 to 7 of the matrix instruction are their
-// high parts, rows 8 to 15 their low parts, so one instruction and one load per
-// lane serve both. An expert with more entries has its rows read again, from
+// Tokens go in groups of eight: the even rows of the matrix instruction are
+// their high parts, the odd rows their low parts, so one instruction and one
+// load per lane serve both. An expert with more entries has its rows read again, from
 // the L2 that this wave has just filled. NG groups share a pass over the rows.
 // A wave's chunks form one stream over all its units, one chunk ahead.
 // Waves per workgroup: 8 of up to 256 registers each; with one row tile and
@@ -789,8 +843,11 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
   extern __shared__ float part[];  // [parts][n][RT * 16]
   __shared__ uint32_t experts_lds[EP_MOE_MAX_ENTRIES];
   __shared__ uint16_t order_lds[EP_MOE_MAX_ENTRIES];
+  __shared__ __attribute__((aligned(16))) char turn_lds[kDownWaves * kTurnBytes];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = lane_id(), r = lane & 15, g = lane >> 4;
+  const int piece_of = near_piece(), step_of = lane & 3;
+  char *const slot = turn_lds + wave * kTurnBytes;
   const int n = T * K, steps = (I + kStep - 1) / kStep, groups = I / kStep;
   const int experts = __builtin_amdgcn_readfirstlane(*active);
   for (int i = threadIdx.x; i < n; i += kDownWaves * kWave) {
@@ -808,7 +865,8 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
   struct Place {  // of a chunk in the stream: unit, first entry of the group, step
     int u, p, s, e, begin, have, s0, s1;
   };
-  const auto enter = [&](Place &a) {  // the unit a.u
+  const auto enter = [&](Place &a) {  // the unit a.u; behind the last one a place whose loads lie outside
+    a.e = a.begin = a.have = a.p = a.s = a.s0 = a.s1 = 0;
     if (a.u >= units) return;
     const int j = a.u / parts, q = a.u - j * parts;
     const MoeEntry m{(uint32_t)__builtin_amdgcn_readfirstlane((int)experts_lds[j])};
@@ -838,7 +896,7 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
     uint32_t wrow[RT], srow[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int at = rt * kTile + r;
+      const int at = rt * kTile + near_row();
       wrow[rt] = at < here ? (uint32_t)(((int64_t)(n0 + at) * I * W::kStepBytes) / kStep) : kOutside;
       srow[rt] = at < here ? (uint32_t)(n0 + at) * (uint32_t)groups * 4u : kOutside;
     }
@@ -851,24 +909,24 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int l = 0; l < W::kLoads; ++l)
-            c.w[u][rt][l] = load16(m.w, weight_at<WT>(I, wrow[rt], a.s + u, a.s1, l, g));
+            c.w[u][rt][l] = load16(m.w, weight_at<WT>(I, wrow[rt], a.s + u, a.s1, l, piece_of));
       if constexpr (W::kScaled) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          c.scale[rt] = load4(m.scales, g < U && a.s + g < a.s1 ? srow[rt] + (uint32_t)(a.s + g) * 4u : kOutside);
+          c.scale[rt] = load4(m.scales, only(step_of < U && a.s + step_of < a.s1,
+                                              srow[rt] + (uint32_t)(a.s + step_of) * 4u));
       }
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng) {
-        const int p = a.p + ng * 8 + (r & 7);
-        const uint32_t tok = p < a.have ? ((uint32_t)order_lds[a.begin + p] * 2u + (r >> 3)) * (uint32_t)I * 2u : kOutside;
+        const int p = a.p + ng * 8 + (r >> 1);
+        const uint32_t tok = only(p < a.have, (uint32_t)((a.begin + p) * 2 + (r & 1)) * 16u);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int s = a.s + u, k = s * kStep + W::place(j, g);
-            uint32_t off = s < a.s1 ? tok + (uint32_t)k * 2u : kOutside;
-            if constexpr (!W::kScaled) off = k < I ? off : kOutside;
-            c.t[u][ng][j] = load16(hb, off);
+            const bool in = s < a.s1 && (W::kScaled || k < I);
+            c.t[u][ng][j] = load16(hb, only(in, tok + (uint32_t)(k >> 3) * (uint32_t)n * 32u));
           }
       }
     };
@@ -878,15 +936,21 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) acc[ng][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // Steps behind the part's end are zeros and not skipped: a load that no use waits for holds
+      // up the next one to its registers.
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (u > 0 && a.s + u >= a.s1) break;
+        u32x4 turned[RT][W::kLoads];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int l = 0; l < W::kLoads; ++l) turned[rt][l] = turn(slot, c.w[u][rt][l]);
         f32x4 sum[NG][RT];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const bf16x8 b = W::operand(c.w[u][rt], j);
+            const bf16x8 b = W::operand(turned[rt], j);
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng) {
               const bf16x8 t = __builtin_bit_cast(bf16x8, c.t[u][ng][j]);
@@ -900,7 +964,7 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
         if constexpr (W::kScaled) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const float sc = lane_value(c.scale[rt], u * 16 + r);
+            const float sc = lane_value(c.scale[rt], r * 4 + u);
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -909,36 +973,34 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
         }
       }
       if (a.s + U < a.s1) return;
-      // the group's end: high and low parts are 32 lanes apart
+      // the group's end: a lane's four results are the parts of two entries
       float *const to = part + (int64_t)(a.u % parts) * n * (RT * kTile);
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = a.p + ng * 8 + (g & 1) * 4 + i;
-          const bool in = g < 2 && p < a.have;
-          const int entry = in ? order_lds[a.begin + p] : 0;
+        for (int i = 0; i < 2; ++i) {
+          const int p = a.p + ng * 8 + g * 2 + i;
+          if (p >= a.have) continue;
+          const int entry = order_lds[a.begin + p];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const float v = acc[ng][rt][i], both = v + lane_value(v, lane ^ 32);
-            if (in) to[entry * (RT * kTile) + rt * kTile + r] = both;
-          }
+          for (int rt = 0; rt < RT; ++rt)
+            to[entry * (RT * kTile) + rt * kTile + r] = acc[ng][rt][2 * i] + acc[ng][rt][2 * i + 1];
         }
     };
     Place a, b;
     a.u = wave;
     enter(a);
     Chunk ca, cb;
-    if (a.u < units) load(ca, a);
+    load(ca, a);
     while (a.u < units) {
       b = next(a);
-      if (b.u < units) load(cb, b);
+      load(cb, b);
       __builtin_amdgcn_sched_barrier(0);
       add(ca, a);
       __builtin_amdgcn_sched_barrier(0);
       if (b.u >= units) break;
       a = next(b);
-      if (a.u < units) load(ca, a);
+      load(ca, a);
       __builtin_amdgcn_sched_barrier(0);
       add(cb, b);
       __builtin_amdgcn_sched_barrier(0);
@@ -1008,7 +1070,7 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
 // The wide kernel reads x once for 128 rows and walks the whole long axis: right
 // where its workgroups fill the chip (256 of them), or come near it and the
 // split kernel would read every matrix again for each 16 of many rows: 16
-// experts of 64 rows, 2048 to 1024 in bf16 (128 workgroups), 51 against 92 us.
+// experts of 64 rows, 2048 to 1024 in bf16 (128 workgroups), 40 against 92 us.
 // Else waves that share the long axis are faster: one row of an fp4 matrix 7168
 // to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 40 against 70,
 // 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 12 against 15.
@@ -1078,8 +1140,9 @@ int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int 
 // 8 bf16 experts of one token, 256 workgroups: 80 us either way), else 16 and
 // the long axis shared (one bf16 expert, 32 workgroups: 18 against 54 us).
 // Second launch: two groups of eight tokens a pass where experts have more than
-// eight entries on the average (64 fp4 experts, 16 entries each: 393 against
-// 434 us), else one (197 active experts, 5 entries each: 619 against 655).
+// eight entries on the average (64 fp4 experts, 16 entries each: 255 against
+// 266 us; 16 fp8 experts of 64: 191 against 237), else one (197 active fp4
+// experts, 5 entries each: 473 against 528).
 template <int WT>
 int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   const int n = a.T * a.K;
@@ -1089,8 +1152,10 @@ int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
                                              : moe_up_split_launch<WT>(a, ws, cap);
   if (rc != 0) return rc;
   // Output rows per workgroup: an even share of the chip's 256 compute units, at most two tiles.
+  // Rounded up to two rows, not to a tile: a small layer fills more compute units (whole layers of
+  // H 256, 336 and 1152: 36.2, 16.5 and 20.0 us; to four rows 36.4, 17.6, 21.2, to 16 40.4, 25.1, 24.8).
   int rows = (a.H + kComputeUnits - 1) / kComputeUnits;
-  rows = (rows + 3) / 4 * 4;
+  rows = (rows + 1) / 2 * 2;
   rows = rows < 2 * kTile ? rows : 2 * kTile;
   const bool many = n > 8 * a.E;
   if (rows <= kTile)
