@@ -1068,18 +1068,21 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
 }
 
 // The wide kernel reads x once for 128 rows and walks the whole long axis: right
-// where its workgroups fill the chip (256 of them), or come near it and the
-// split kernel would read every matrix again for each 16 of many rows: 16
-// experts of 64 rows, 2048 to 1024 in bf16 (128 workgroups), 40 against 92 us.
+// where its workgroups take most compute units (24 fp8 experts of 4 rows, 4096
+// to 1024, 192 workgroups: 20 against 48 us; one fp4 row to 14336, 112: 23
+// against 32; 12 experts of a row, 96: 17 against 19 in fp8, 21 against 20 in
+// bf16), or a fifth of them and the split kernel would read every matrix again
+// for each 16 of more rows (one bf16 expert of 64 rows, 7168 to 7168, 56
+// workgroups: 83 against 114; 3 experts of 29, 39 workgroups: 34 against 35).
 // Else waves that share the long axis are faster: one row of an fp4 matrix 7168
-// to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 40 against 70,
-// 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 12 against 15.
+// to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 41 against 60,
+// 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 11 against 15.
 template <int WT>
 int matvec_pick(const ExpertMatvecArgs &a, int cap) {
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
   const int64_t wide_tiles = (a.N + 4 * kWideTiles * kTile - 1) / (4 * kWideTiles * kTile);
   const int64_t units = experts * wide_tiles;
-  const bool wide = units >= kComputeUnits || (units >= kComputeUnits / 4 && a.capacity > 32 * experts);
+  const bool wide = units >= kComputeUnits * 3 / 8 || (units >= kComputeUnits / 5 && a.capacity > kTile * experts);
   return wide ? matvec_wide_launch<WT>(a, cap) : matvec_split_launch<WT>(a, cap);
 }
 
@@ -1137,8 +1140,12 @@ int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int 
 
 // First launch: 64 channels a workgroup where these fill the chip (28 fp8
 // entries of 20 experts, hidden 2048, 240 to 336 workgroups: 15 against 20 us;
-// 8 bf16 experts of one token, 256 workgroups: 80 us either way), else 16 and
-// the long axis shared (one bf16 expert, 32 workgroups: 18 against 54 us).
+// 8 bf16 experts of one token, 256 workgroups: 80 us either way), or half of it
+// with four entries an expert (128 workgroups in bf16, hidden 4096: 25 against
+// 27 us with 4 entries an expert, 28 against 37 with 16), else 16 and the long
+// axis shared (8 fp4 experts of one token, 176 workgroups: 16 against 18 us; 4
+// fp8 experts of 32 entries, 64: 29 against 38; one bf16 expert, 32: 18 against
+// 54).
 // Second launch: two groups of eight tokens a pass where experts have more than
 // eight entries on the average (64 fp4 experts, 16 entries each: 255 against
 // 266 us; 16 fp8 experts of 64: 191 against 237), else one (197 active fp4
@@ -1147,9 +1154,10 @@ template <int WT>
 int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   const int n = a.T * a.K;
   constexpr int kChannels = kWideTiles / 2 * 4 * kTile;
-  const int64_t wide_units = (int64_t)(n < a.E ? n : a.E) * ((a.I + kChannels - 1) / kChannels);
-  const int rc = wide_units >= kComputeUnits ? moe_up_wide_launch<WT>(a, ws, cap)
-                                             : moe_up_split_launch<WT>(a, ws, cap);
+  const int experts = n < a.E ? n : a.E;
+  const int64_t wide_units = (int64_t)experts * ((a.I + kChannels - 1) / kChannels);
+  const bool wide = wide_units >= kComputeUnits || (wide_units >= kComputeUnits / 2 && n >= 4 * experts);
+  const int rc = wide ? moe_up_wide_launch<WT>(a, ws, cap) : moe_up_split_launch<WT>(a, ws, cap);
   if (rc != 0) return rc;
   // Output rows per workgroup: an even share of the chip's 256 compute units, at most two tiles.
   // Rounded up to two rows, not to a tile: a small layer fills more compute units (whole layers of
