@@ -23,7 +23,7 @@
 // launch of one token).
 // Measured on MI355X: a bf16 layer of one token, top-8, hidden 7168,
 // intermediate 2048 (705 MB of weights) 123 us, 5.7 TB/s; 128 tokens over 197
-// active fp4 experts of 256 (4.6 GB) 1046 us, 4.4 TB/s; fp4 products of 1024
+// active fp4 experts of 256 (4.6 GB) 1000 to 1046 us, 4.5 TB/s; fp4 products of 1024
 // rows over 64 experts, 7168 to 4096 (1.0 GB) 207 us, 4.9 TB/s.
 #include <type_traits>
 

@@ -233,6 +233,13 @@ LAYER = [
     (120, 8, 20, 128, 896, "fp8", 0.0, False, False, False),  # 48 entries per expert
     (40, 4, 64, 640, 256, "fp4", 0.1, True, True, False),
     (4, 2, 64, 4096, 2048, "fp4", 0.0, False, True, False),  # 8 entries, 32 tiles each
+    # two row tiles in the second launch, parts of the long axis that end inside a chunk
+    (4, 2, 16, 7168, 640, "fp4", 0.0, False, True, True),
+    (4, 2, 16, 4480, 640, "fp8", 0.1, False, True, False),
+    (3, 2, 8, 4360, 200, "bf16", 0.0, False, True, True),
+    (40, 8, 8, 4360, 136, "bf16", 0.1, False, True, False),  # 40 entries per expert
+    (40, 8, 8, 4480, 384, "fp8", 0.0, True, True, True),
+    (70, 7, 30, 4480, 896, "fp4", 0.2, True, True, False),  # 13 entries per expert
 ]
 
 
