@@ -451,9 +451,9 @@ size_t ep_moe_layer_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t in
  *   h           = gate / (1 + exp(-gate)) * up
  *   out[t]      = sum over k of topk_weights[t, k] * (w_out[e] h)  (+ bias[t])
  * in binary32 with the k in ascending order, rounded once to bf16; h is
- * carried as a sum of two bf16 values (2^-17 relative). An id may occur
- * twice in a token: both entries count. A token without unmasked entries
- * gets bias[t], or +0.
+ * carried as a sum of two bf16 values (2^-17 relative), so an infinite weight
+ * or scale of w_out gives NaN. An id may occur twice in a token: both entries
+ * count. A token without unmasked entries gets bias[t], or +0.
  *
  *   x             bf16 [num_tokens, hidden]
  *   topk_idx      int32 [num_tokens, topk]
