@@ -20,9 +20,10 @@
 // on their way into registers, one in the other half of LDS, and loads and LDS
 // stores are issued between the matrix instructions of a step (all at its
 // start: 11% slower).
-// Measured on MI355X: 64 experts of 128 e4m3 rows 1047 us (3.7 TB/s), 8
-// experts of 2048 bf16 rows, 4096 by 2048, added to an fp32 gradient 338 us
-// (813 TFLOP/s).
+// Measured on MI355X: 64 experts of 128 e4m3 rows 965 us (4.0 TB/s), with
+// scales that are no powers of two (three products for every one, below) 2355;
+// 8 experts of 2048 rows, 4096 by 2048, added to an fp32 gradient, 308 us in
+// bf16 (890 TFLOP/s), 315 in e4m3 and 927 with scales of any kind.
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -58,6 +59,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
                                            kRawBufferFlags);
 }
 
+// The same in every lane, said so: a descriptor that the compiler takes for a lane's own costs a loop
+// around every access and registers (8 experts of 2048 bf16 rows 331 us against 308, and spills).
+__device__ __forceinline__ const char *uniform(const char *p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return (const char *)((uint64_t)hi << 32 | lo);
+}
+
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const f32x2 f = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
@@ -72,6 +82,28 @@ __device__ __forceinline__ bf16x8 column(const char *upper, const char *lower) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Values of x = code * scale (e4m3 rows) as the matrix cores take them. Codes
+// are exact in bf16, and so are their products with a power of two between
+// 2^-64 and 2^64. Any other scale leaves up to 24 bits after the binary32
+// product, which are three bf16 parts, each the upper half of what the ones
+// before leave; with a product for each part nothing but bits below 2^-133
+// (bf16's least step) is lost. Rounding x to bf16 instead would put the
+// gradient of 128 rows with scales in [0.01, 1] off by 1.7e-3 where the sum in
+// binary32 is off by 2e-7. What the scales are is found on the way: a tile is
+// begun with one product, and begun again with three where a value was rounded.
+__device__ __forceinline__ void three_parts(float p, uint32_t (&part)[3]) {  // in the upper halves
+#pragma clang fp contract(off)  // p is one rounded value: fused with its product, the parts could come from two
+  part[0] = __float_as_uint(p);
+  const float rest = p - __uint_as_float(part[0] & 0xFFFF0000u);
+  part[1] = __float_as_uint(rest);
+  part[2] = __float_as_uint(rest - __uint_as_float(part[1] & 0xFFFF0000u));
+  if ((part[0] & 0x7F800000u) == 0x7F800000u) {  // an infinity or NaN is all in the first part
+    part[0] |= (part[0] & 0x007FFFFFu) != 0 ? 0x00400000u : 0u;
+    part[1] = part[2] = 0;
+  }
+}
+__device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) { return lo >> 16 | (hi & 0xFFFF0000u); }
+
 // One step's rows on the way from memory to LDS, in a thread's registers: it
 // takes the same 16-byte pieces of every step (two of dy, then those of x), at
 // offsets from the step's first row that are found once per tile.
@@ -84,6 +116,7 @@ struct Stage {
   u32x4 v[2][kPieces];
   float scale[2][kPiecesX];
   bool scaled;
+  bool rounded = false;  // a value of x in the pieces stored so far was (the same in all lanes)
 
   static __device__ __forceinline__ int row_y(int i) { return (threadIdx.x + i * kThreads) / (kTileN / 8); }
   static __device__ __forceinline__ int col_y(int i) { return (threadIdx.x + i * kThreads) % (kTileN / 8) * 8; }
@@ -107,11 +140,12 @@ struct Stage {
   // rows (the stream's end) touch no memory.
   __device__ __forceinline__ void aim(const char *y, const char *x, const char *s, int rows, int N,
                                       int H, bool with_scales) {
-    by = buffer_of(y, (int64_t)(rows * N) * 2);
-    bx = buffer_of(x, (int64_t)(rows * H) * (FP8 ? 1 : 2));
+    rows = __builtin_amdgcn_readfirstlane(rows);
+    by = buffer_of(uniform(y), (int64_t)(rows * N) * 2);
+    bx = buffer_of(uniform(x), (int64_t)(rows * H) * (FP8 ? 1 : 2));
     if constexpr (FP8) {
       scaled = with_scales;
-      bs = buffer_of(s, scaled ? rows * (H / 128) * 4 : 0);
+      bs = buffer_of(uniform(s), scaled ? rows * (H / 128) * 4 : 0);
     }
   }
   __device__ __forceinline__ void load(int set, int i) {
@@ -126,36 +160,69 @@ struct Stage {
     *(u32x2 *)to = u32x2{w[0], w[1]};
     *(u32x2 *)(to + kPlaneX) = u32x2{w[2], w[3]};
   }
-  __device__ __forceinline__ void store(int set, int i, char *ly, char *lx) const {
+  __device__ __forceinline__ void store(int set, int i, char *ly, char *lx) {
     if (i < 2) {
       *(u32x4 *)(ly + row_y(i) * kStrideY + col_y(i) * 2) = v[set][i];
     } else if constexpr (FP8) {
-      // A power of two between 2^-64 and 2^64 leaves every value exact in bf16: one instruction
-      // converts two values. Other scales (of any lane of the wave) multiply in binary32 and round.
+      // One instruction converts two values where every lane of the wave can: rows behind the end
+      // and groups of zeros (codes 0 and a finite scale) count as scaled by 1. Other scales multiply
+      // in binary32 and round; values that this changes are noted, but for those below 2^-126, whose
+      // bits bf16 cannot hold in any number of parts.
       const u32x4 c = v[set][i];
-      const float s = scaled ? scale[set][i - 2] : 1.0f;
+      float s = scaled ? scale[set][i - 2] : 1.0f;
+      if ((c[0] | c[1] | c[2] | c[3]) == 0 && (__float_as_uint(s) & 0x7F800000u) != 0x7F800000u) s = 1.0f;
       const uint32_t bits = __float_as_uint(s);
-      const bool exact = (bits & 0x807FFFFFu) == 0 && bits >= 0x1F800000u && bits <= 0x5F800000u;
+      const bool direct = (bits & 0x807FFFFFu) == 0 && bits >= 0x1F800000u && bits <= 0x5F800000u;
       u32x4 w[2];
-      if (ballot(!exact) == 0) {
+      if (ballot(!direct) == 0) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           w[d >> 1][(d & 1) * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, false));
           w[d >> 1][(d & 1) * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, true));
         }
       } else {
+        uint32_t lost = 0;
+        const auto two = [&](f32x2 q) {
+          const uint32_t lo = __float_as_uint(q[0] * s), hi = __float_as_uint(q[1] * s);
+          lost |= ((lo & 0x7F800000u) != 0 ? lo & 0xFFFFu : 0u) | ((hi & 0x7F800000u) != 0 ? hi & 0xFFFFu : 0u);
+          return pack(__uint_as_float(lo), __uint_as_float(hi));
+        };
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], false);
-          const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], true);
-          w[d >> 1][(d & 1) * 2] = pack(lo[0] * s, lo[1] * s);
-          w[d >> 1][(d & 1) * 2 + 1] = pack(hi[0] * s, hi[1] * s);
+          w[d >> 1][(d & 1) * 2] = two(__builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], false));
+          w[d >> 1][(d & 1) * 2 + 1] = two(__builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], true));
         }
+        rounded = rounded || ballot(lost != 0) != 0;
       }
       put_x(lx, row_x(i - 2), col_x(i - 2), w[0]);
       put_x(lx, row_x(i - 2), col_x(i - 2) + 8, w[1]);
     } else {
       put_x(lx, row_x(i - 2), col_x(i - 2), v[set][i]);
+    }
+  }
+  // e4m3 rows: the three parts of x to three places.
+  __device__ __forceinline__ void store_parts(int set, int i, char *ly, char *lx) const {
+    if (i < 2) {
+      *(u32x4 *)(ly + row_y(i) * kStrideY + col_y(i) * 2) = v[set][i];
+      return;
+    }
+    const u32x4 c = v[set][i];
+    const float s = scale[set][i - 2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // eight values
+      u32x4 w[3];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const f32x2 q = (d & 1) == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[2 * half + (d >> 1)], false)
+                                     : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[2 * half + (d >> 1)], true);
+        uint32_t lo[3], hi[3];
+        three_parts(q[0] * s, lo);
+        three_parts(q[1] * s, hi);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) w[t][d] = upper_halves(lo[t], hi[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) put_x(lx + t * (kRows * kStrideX), row_x(i - 2), col_x(i - 2) + 8 * half, w[t]);
     }
   }
 };
@@ -168,8 +235,11 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
   using Rows = Stage<FP8>;
   constexpr int kPieces = Rows::kPieces, kElt = FP32 ? 4 : 2;
   constexpr int kTilesQ = kTileH / 32;  // 16-column tiles of x per wave
-  __shared__ __attribute__((aligned(16))) char lds[2][kRows * (kStrideY + kStrideX)];
-  static_assert(kThreads / kWave * 16 * kStrideOut <= (int)sizeof lds, "the way out fits the steps' LDS");
+  constexpr int kStepBytes = kRows * (kStrideY + kStrideX);
+  constexpr int kLdsBytes = FP8 ? kRows * (kStrideY + 3 * kStrideX) : 2 * kStepBytes;  // two steps, or one in parts
+  static_assert(kLdsBytes >= 2 * kStepBytes && kThreads / kWave * 16 * kStrideOut <= kLdsBytes,
+                "every use fits the LDS, two workgroups a compute unit");
+  __shared__ __attribute__((aligned(16))) char lds[kLdsBytes];
   const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wn = (wave & 1) * 64, wh = (wave >> 1) * (kTileH / 2);
@@ -177,6 +247,14 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
   const int row = g * 4 + (r16 >> 2);
   const int at_y = row * kStrideY + wn * 2 + (r16 & 3) * 8;
   const int at_x = kRows * kStrideY + row * kStrideX + wh / 2 + (r16 & 1) * 2 * kPlaneX + (r16 >> 1 & 1) * 8;
+  // Whether a wave has rounded a value of x in the first step, and in a later one: two sets in turn, so
+  // that one is cleared while no wave can still read or write it.
+  __shared__ int rounded[2][2];
+  int turn = 0;
+  if constexpr (FP8) {
+    if (threadIdx.x < 4) rounded[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+    __syncthreads();
+  }
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     // Workgroup u runs on XCD u % 8: each XCD takes one eighth of every expert's tiles, so what
     // they share of dy and x is in its own L2, whatever the experts' sizes.
@@ -193,6 +271,7 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
       else if (count > capacity - begin) count = (int)(capacity - begin);
     }
     f32x4 acc[4][kTilesQ];
+    bool in_parts = false;  // the same in every wave
     if (count > 0) {
       Rows stage;
       stage.place(N, H, n0, h0);
@@ -217,14 +296,23 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
       aim();
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        stage.store(0, i, lds[0], lds[0] + kRows * kStrideY);
+        stage.store(0, i, lds, lds + kRows * kStrideY);
         stage.load(0, i);
       }
+      int *const seen = rounded[turn];
+      if constexpr (FP8)
+        if (stage.rounded) seen[0] = 1;
       __syncthreads();
+      if constexpr (FP8) {
+        turn ^= 1;  // every wave has left the last tile: its set is free
+        if (threadIdx.x < 2) rounded[turn][threadIdx.x] = 0;
+      }
       const auto step = [&](auto set, auto first) {  // products of the step in lds[set]
+        if constexpr (FP8)
+          if (stage.rounded) seen[1] = 1;  // in the steps stored so far; the last one stores rows behind the end
         aim();
-        const char *sy = lds[set] + at_y, *sx = lds[set] + at_x;
-        char *to = lds[set ^ 1];
+        const char *sy = lds + set * kStepBytes + at_y, *sx = lds + set * kStepBytes + at_x;
+        char *to = lds + (set ^ 1) * kStepBytes;
         // tile q holds, as row 4a + b, column 32 (q / 2) + 8a + 4 (q % 2) + b: two tiles give a
         // lane eight consecutive columns of a row of the gradient
         const auto column_x = [&](int q) {
@@ -252,9 +340,13 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
       constexpr std::integral_constant<int, 0> even{};
       constexpr std::integral_constant<int, 1> odd{};
       step(even, std::true_type());
-      for (int rows = count - kRows; rows > 0; rows -= 2 * kRows) {
-        step(odd, std::false_type());
-        if (rows > kRows) step(even, std::false_type());
+      if constexpr (FP8) in_parts = __builtin_amdgcn_readfirstlane(seen[0]) != 0;
+      if (!in_parts) {
+        for (int rows = count - kRows; rows > 0; rows -= 2 * kRows) {
+          step(odd, std::false_type());
+          if (rows > kRows) step(even, std::false_type());
+        }
+        if constexpr (FP8) in_parts = __builtin_amdgcn_readfirstlane(seen[1]) != 0;
       }
     } else {
 #pragma unroll
@@ -262,9 +354,55 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
 #pragma unroll
         for (int q = 0; q < kTilesQ; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    if constexpr (FP8) {
+      if (in_parts) {  // again, with three products for every one: a step's parts of x side by side in LDS
+        Rows stage;
+        stage.place(N, H, n0, h0);
+        int left = count;
+        const char *from_y = dy + begin * N * 2, *from_x = x + begin * H;
+        const char *from_s = (const char *)(x_scales + begin * (H / 128));
+        const auto fetch = [&] {
+          stage.aim(from_y, from_x, from_s, left <= 0 ? 0 : (left < kRows ? left : kRows), N, H, true);
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) stage.load(0, i);
+          left -= kRows;
+          from_y += (int64_t)kRows * N * 2;
+          from_x += (int64_t)kRows * H;
+          from_s += (int64_t)kRows * (H / 128) * 4;
+        };
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int q = 0; q < kTilesQ; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        fetch();
+        for (int rows = count; rows > 0; rows -= kRows) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) stage.store_parts(0, i, lds, lds + kRows * kStrideY);
+          __syncthreads();
+          fetch();
+          bf16x8 b[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) b[p] = column(lds + at_y + p * 32, lds + at_y + p * 32 + 16 * kStrideY);
+#pragma unroll 1
+          for (int t = 0; t < 3; ++t) {
+            const char *sx = lds + at_x + t * (kRows * kStrideX);
+#pragma unroll
+            for (int q = 0; q < kTilesQ; ++q) {
+              const char *at = sx + (q >> 1) * 16 + (q & 1) * kPlaneX;
+              const bf16x8 a = column(at, at + 16 * kStrideX);
+#pragma unroll
+              for (int p = 0; p < 4; ++p)
+                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[p], acc[p][q], 0, 0, 0);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          __syncthreads();
+        }
+      }
+    }
     // Results leave as whole 128-byte lines: 16 rows of 64 columns at a time pass through LDS
     // (each wave its own part), from where 8 (bf16) or 16 lanes take a row.
-    char *const mine = lds[0] + wave * 16 * kStrideOut;
+    char *const mine = lds + wave * 16 * kStrideOut;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const int n = n0 + wn + p * 16, rows = N - n < 16 ? N - n : 16;

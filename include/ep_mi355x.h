@@ -537,9 +537,11 @@ int ep_swiglu_backward(const void *dh, const void *checkpoint, const float *chec
  * Weight gradient of the experts' products:
  *   dw[e] = previous[e] + sum over the rows r of expert e of dy[r]^T x[r]
  * with x kept in bf16 or in 8 bits (rows as dispatch moves them, or a
- * checkpoint): x[r] = code * x_scales[r], rounded to bf16, which is exact for
- * power-of-two scales such as ep_swiglu's. Summed in binary32, rounded once.
- * An expert without rows gets previous[e], or zeros.
+ * checkpoint): x[r] = code * x_scales[r], rounded to binary32 (and to a
+ * multiple of 2^-133, which matters below 2^-110). Summed in binary32, rounded
+ * once. Scales that are powers of two, such as ep_swiglu's, take one pass of
+ * the matrix cores, others three (64 experts of 128 rows 965 and 2355 us on
+ * MI355X). An expert without rows gets previous[e], or zeros.
  *
  *   dy          bf16 [capacity_rows, out_features]
  *   x           bf16 or e4m3 (x_dtype) [capacity_rows, in_features]
