@@ -99,6 +99,15 @@ __device__ __forceinline__ int wave_inclusive_scan(int x) {
   return x + (lane >= 16 ? r0 : 0) + (lane >= 32 ? r1 : 0) + (lane >= 48 ? r2 : 0);
 }
 
+// Cuts an expert's span to the rows inside a buffer of `capacity` rows (below
+// 2^31): returns their number (below 1: none) and leaves the first in `begin`.
+__device__ __forceinline__ int clip_span(int &begin, int count, int64_t capacity) {
+  int64_t end = (int64_t)begin + count;
+  end = end < 0 ? 0 : (end < capacity ? end : capacity);
+  begin = begin < 0 ? 0 : begin;
+  return (int)(end - begin);
+}
+
 // Sum over the 64 lanes of a wavefront (the same value in every lane).
 __device__ __forceinline__ int wave_sum(int x) {
   x = row_inclusive_scan(x);

@@ -453,13 +453,12 @@ __device__ __forceinline__ Segment find_segment(int j, const int32_t *__restrict
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int e = first + q * kWave + lane;
-      begin[q] = e < E ? offsets[e] : -1;
+      begin[q] = e < E ? offsets[e] : 0;
       count[q] = e < E ? counts[e] : 0;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (begin[q] < 0 || begin[q] >= capacity) count[q] = 0;
-      else if (count[q] > capacity - begin[q]) count[q] = (int)(capacity - begin[q]);
+      count[q] = clip_span(begin[q], count[q], capacity);
       const uint64_t have = ballot(count[q] > 0);
       const int n = __builtin_popcountll(have);
       if (s.e < 0 && j < n) {

@@ -265,10 +265,9 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
     int64_t begin = 0;
     int count = (int)capacity;
     if (counts != nullptr) {
-      begin = __builtin_amdgcn_readfirstlane(offsets[e]);
-      count = __builtin_amdgcn_readfirstlane(counts[e]);
-      if (begin < 0 || begin >= capacity || count < 0) count = 0;
-      else if (count > capacity - begin) count = (int)(capacity - begin);
+      int first = __builtin_amdgcn_readfirstlane(offsets[e]);
+      count = clip_span(first, __builtin_amdgcn_readfirstlane(counts[e]), capacity);
+      begin = first;
     }
     f32x4 acc[4][kTilesQ];
     bool in_parts = false;  // the same in every wave
