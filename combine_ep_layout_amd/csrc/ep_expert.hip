@@ -823,17 +823,16 @@ __global__ __launch_bounds__(kThreads, 2) void ep_moe_up_wide(
 // A wave's chunks form one stream over all its units, one chunk ahead.
 // Waves per workgroup: 8 of up to 256 registers each; with one row tile and
 // half the chunk a wave needs half as many, and 16 waves are faster (45 tokens,
-// hidden 336: 18 against 21 us).
+// hidden 336: 18 against 21 us). out may be bias, so neither is __restrict__.
 constexpr int down_waves(int row_tiles, int groups) { return row_tiles == 1 && groups == 1 ? 16 : 8; }
 
 template <int WT, int RT, int NG>
 __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
     const uint16_t *__restrict__ h, const int32_t *__restrict__ topk_idx,
-    const float *__restrict__ topk_weights, const uint16_t *__restrict__ bias,
+    const float *__restrict__ topk_weights, const uint16_t *bias,
     const void *__restrict__ w, const float *__restrict__ scales, int T, int H, int I, int K, int E,
     int rows, int tiles, int most_parts, const int32_t *__restrict__ active,
-    const uint32_t *__restrict__ list, const uint16_t *__restrict__ order,
-    uint16_t *__restrict__ out) {
+    const uint32_t *__restrict__ list, const uint16_t *__restrict__ order, uint16_t *out) {
   using W = Weights<WT>;
   constexpr int kDownWaves = down_waves(RT, NG);
   constexpr int kChunkBytes = NG == 1 ? (RT == 1 ? 128 : 256) : 128;  // of a weight row

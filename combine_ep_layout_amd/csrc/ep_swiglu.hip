@@ -206,12 +206,12 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
   }
 }
 
+// h may be dh, so neither is __restrict__: a thread loads its channels of dh before it stores h there.
 template <bool FP32, bool WITH_H>
 __global__ __launch_bounds__(kThreads) void ep_swiglu_backward_rows(
-    const char *__restrict__ dh, const char *__restrict__ codes, const float *__restrict__ scales,
+    const char *dh, const char *__restrict__ codes, const float *__restrict__ scales,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int E, int64_t capacity,
-    int I, int block_rows, int64_t blocks, FastDiv by_chunks, char *__restrict__ d_gate_up,
-    char *__restrict__ h) {
+    int I, int block_rows, int64_t blocks, FastDiv by_chunks, char *__restrict__ d_gate_up, char *h) {
   __shared__ uint32_t lds;
   constexpr int kElt = Row<FP32>::kElt;
   const int chunks = I / kLane;
