@@ -99,6 +99,16 @@ __device__ __forceinline__ int wave_inclusive_scan(int x) {
   return x + (lane >= 16 ? r0 : 0) + (lane >= 32 ? r1 : 0) + (lane >= 48 ? r2 : 0);
 }
 
+// 1 / (1 + exp(-z)) for z below kFarGate, where the result, and soon exp(-z),
+// leaves binary32's normal numbers while z * sigmoid(z) * up need not: exp(z) in
+// binary64 (1 + exp(z) is 1), as the square of exp(z / 2). Rare, so accurate
+// rather than fast; exp(87) is 6.1e37 and exp(-87) 1.6e-38, both normal.
+constexpr float kFarGate = -87.0f;
+__device__ __forceinline__ double far_sigmoid(float z) {
+  const double a = expf(0.5f * z);
+  return a * a;
+}
+
 // Cuts an expert's span to the rows inside a buffer of `capacity` rows (below
 // 2^31): returns their number (below 1: none) and leaves the first in `begin`.
 __device__ __forceinline__ int clip_span(int &begin, int count, int64_t capacity) {

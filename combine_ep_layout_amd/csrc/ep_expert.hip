@@ -706,7 +706,8 @@ __device__ __forceinline__ void note_expert(int j, int e, const FindLds &f, int3
 // second launch's lanes, a part of an entry each, then read consecutive pieces of
 // 16 bytes.
 __device__ __forceinline__ void put_h(uint16_t *h, int n, int at, int c, float gate, float up) {
-  const float v = silu(gate) * up;
+  // below kFarGate the sigmoid is the square of a = exp(gate / 2), which stays a normal number
+  const float a = __expf(0.5f * gate), v = gate < kFarGate ? up * a * gate * a : silu(gate) * up;
   const uint16_t hi = bf16_bits(v);
   uint16_t *to = h + ((int64_t)(c >> 3) * n + at) * 16 + (c & 7);
   to[0] = hi;

@@ -36,13 +36,20 @@ constexpr int kLane = 8;      // channels per lane
 constexpr int kMaxRows = 32;  // rows per block: bits of the mask
 constexpr int kCodePolicy = 2 | 16;  // nt, sc1
 
-// 1 / (1 + exp(-z)). EXACT (binary32 rows) uses the accurate exponential and
+// 1 / (1 + exp(-z)) for z from kFarGate on. EXACT (binary32 rows) uses the accurate exponential and
 // division; bf16 rows the hardware's exp2 and reciprocal, whose error (about
 // 2^-22 for |z| below 8, 2^-19 at 80) is far below half a bf16 step.
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (EXACT) return 1.0f / (1.0f + expf(-z));
   else return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+__device__ __forceinline__ float least(const float (&v)[kLane]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < kLane; ++i) m = fminf(m, v[i]);
+  return m;
 }
 
 // Stores are non-temporal, those of 16-byte pieces that fill whole lines at
@@ -190,6 +197,11 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
       Row<FP32>::load(gate_up + (row * 2 * I + I + i) * kElt, u);
 #pragma unroll
       for (int q = 0; q < kLane; ++q) v[q] = g[q] * sigmoid<FP32>(g[q]) * u[q];
+      if (least(g) < kFarGate) {
+#pragma unroll
+        for (int q = 0; q < kLane; ++q)
+          if (g[q] < kFarGate) v[q] = (float)(g[q] * far_sigmoid(g[q]) * u[q]);
+      }
       Row<FP32>::store(to_h, (r * I + i) * kElt, v);
       if constexpr (SAVE) {
         float sg, su;
@@ -234,12 +246,24 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_backward_rows(
       Row<FP32>::load(dh + (row * I + i) * kElt, d);
       dequantize(cg, sc[0], g);
       dequantize(cu, sc[I / 128], u);
-#pragma unroll
-      for (int q = 0; q < kLane; ++q) {
+      const auto near = [&](int q) {
         const float s = sigmoid<FP32>(g[q]), gs = g[q] * s;
         dg[q] = d[q] * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
         du[q] = d[q] * gs;
         if constexpr (WITH_H) v[q] = gs * u[q];
+      };
+      const auto far = [&](int q) {
+        const double s = far_sigmoid(g[q]), gs = g[q] * s;
+        dg[q] = (float)(s * u[q] * d[q] * (1.0 + g[q] * (1.0 - s)));
+        du[q] = (float)(gs * d[q]);
+        if constexpr (WITH_H) v[q] = (float)(gs * u[q]);
+      };
+      if (least(g) < kFarGate) {
+#pragma unroll
+        for (int q = 0; q < kLane; ++q) g[q] < kFarGate ? far(q) : near(q);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kLane; ++q) near(q);
       }
       Row<FP32>::store(to_d, (r * 2 * I + i) * kElt, dg);
       Row<FP32>::store(to_d, (r * 2 * I + I + i) * kElt, du);

@@ -450,8 +450,9 @@ size_t ep_moe_layer_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t in
  *   [gate | up] = w_in[e] x[t]          (rows [0, I) of w_in are gate's)
  *   h           = gate / (1 + exp(-gate)) * up
  *   out[t]      = sum over k of topk_weights[t, k] * (w_out[e] h)  (+ bias[t])
- * in binary32 with the k in ascending order, rounded once to bf16; h is
- * carried as a sum of two bf16 values (2^-17 relative), so an infinite weight
+ * in binary32 (gates below -87 as in ep_swiglu) with the k in ascending order,
+ * rounded once to bf16; h is carried as a sum of two bf16 values (2^-17
+ * relative; above bf16's largest value it is infinite), so an infinite weight
  * or scale of w_out gives NaN. An id may occur twice in a token: both entries
  * count. A token without unmasked entries gets bias[t], or +0.
  *
@@ -498,7 +499,8 @@ int ep_expert_matvec(const void *x, const void *w, const float *w_scales, const 
  * The experts' gated activation, and an 8-bit checkpoint of its input for
  * ep_swiglu_backward. For the experts' rows [gate | up] of gate_up:
  *   h = gate / (1 + exp(-gate)) * up
- * in binary32, rounded once to the rows' type; and, unless checkpoint and
+ * in binary32, rounded once to the rows' type (a gate below -87, where
+ * 1 / (1 + exp(-gate)) is no normal binary32 number, keeps its h); and, unless checkpoint and
  * checkpoint_scales are NULL, per 128 values of the row the scale 2^p, p the
  * smallest integer >= -126 that keeps the group's largest finite magnitude
  * within 448 * 2^p, and the e4m3 codes of value / 2^p (round to nearest
@@ -520,8 +522,8 @@ int ep_swiglu(const void *gate_up, const int32_t *counts, const int32_t *offsets
  * scale, s = 1 / (1 + exp(-gate)), for the experts' rows
  *   d_gate_up = [dh * up * s * (1 + gate * (1 - s)) | dh * gate * s]
  *   h         = gate * s * up   (unless h is NULL: for the next weight gradient)
- * in binary32, rounded once. Any finite fp32 scales are accepted. With bf16
- * rows, s is taken as 0 where it is below 2^-126 (gate under -87).
+ * in binary32 (gates below -87 as in ep_swiglu), rounded once. Any finite fp32
+ * scales are accepted.
  *
  *   dh          [capacity_rows, intermediate] of dtype (EP_BF16, EP_FP32)
  *   d_gate_up   [capacity_rows, 2 * intermediate] of dtype
