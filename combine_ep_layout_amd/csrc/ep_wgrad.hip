@@ -400,7 +400,8 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
       }
     }
     // Results leave as whole 128-byte lines: 16 rows of 64 columns at a time pass through LDS
-    // (each wave its own part), from where 8 (bf16) or 16 lanes take a row.
+    // (each wave its own part), from where 8 (bf16) or 16 lanes take a row. A wave's LDS accesses
+    // keep their order; the fences keep the compiler's, which sees a lane read and write different places.
     char *const mine = lds + wave * 16 * kStrideOut;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -415,6 +416,7 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *(f32x4 *)(mine + r16 * kStrideOut + (q >> 1) * 128 + g * 32 + (q & 1) * 16) = acc[p][part * 4 + q];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         constexpr int kLanes = FP32 ? 16 : 8, kPasses = 16 * kLanes / kWave;
         u32x4 was[kPasses];
         uint32_t off[kPasses];
@@ -445,6 +447,7 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
           }
           __builtin_amdgcn_raw_buffer_store_b128(w, to, (int)off[i], 0, kNonTemporal);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
     }
     __syncthreads();
