@@ -42,6 +42,7 @@ constexpr uint32_t kOutside = 0x80000000u;  // a buffer offset outside every des
 constexpr int kTile = 16;                   // rows and tokens of one matrix instruction
 constexpr int kStep = 128;                  // values of the long axis per step: one scale group
 constexpr int kThreads = 256;
+constexpr int kComputeUnits = 256;
 constexpr int kWideTiles = 2;               // 16-row tiles per wave of the wide kernels
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
@@ -442,13 +443,15 @@ struct Segment {
   int e;
   int64_t begin, count;
 };
+template <bool ALL = false>  // ALL: also the number of experts that have rows
 __device__ __forceinline__ Segment find_segment(int j, const int32_t *__restrict__ counts,
                                                 const int32_t *__restrict__ offsets, int E,
-                                                int64_t capacity) {
+                                                int64_t capacity, int *have_rows = nullptr) {
   if (counts == nullptr) return {j == 0 ? 0 : -1, 0, capacity};
   const int lane = lane_id();
   Segment s{-1, 0, 0};
-  for (int first = 0; first < E && s.e < 0; first += 4 * kWave) {
+  int total = 0;
+  for (int first = 0; first < E && (ALL || s.e < 0); first += 4 * kWave) {
     int begin[4], count[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -466,9 +469,23 @@ __device__ __forceinline__ Segment find_segment(int j, const int32_t *__restrict
         s = {first + q * kWave + at, read_lane(begin[q], at), read_lane(count[q], at)};
       }
       j -= n;
+      total += n;
     }
   }
+  if constexpr (ALL) *have_rows = total;
   return s;
+}
+
+// Rows of all experts, each one's up to 2^16 of them.
+__device__ __forceinline__ int rows_of_all(const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets,
+                                           int E, int64_t capacity) {
+  int mine = 0;
+  for (int e = lane_id(); e < E; e += kWave) {
+    int begin = offsets[e];
+    const int n = clip_span(begin, counts[e], capacity);
+    mine += n < 0 ? 0 : (n < 1 << 16 ? n : 1 << 16);
+  }
+  return wave_sum(mine);
 }
 
 template <int WT, int MT, bool FP32>
@@ -506,7 +523,83 @@ __device__ __forceinline__ void matvec_wide_group(const Matrix &m, const uint16_
     }
 }
 
-// Many tiles: a workgroup takes 128 rows of one expert's matrix.
+// The wide kernel reads x once for 128 rows and walks the whole long axis: right
+// where its workgroups take most compute units (24 fp8 experts of 4 rows, 4096
+// to 1024, 192 workgroups: 20 against 48 us; one fp4 row to 14336, 112: 23
+// against 32; 12 experts of a row, 96: 17 against 19 in fp8, 21 against 20 in
+// bf16), or a fifth of them and the split kernel would read every matrix again
+// for each 16 of more rows (one bf16 expert of 64 rows, 7168 to 7168, 56
+// workgroups: 83 against 114; 3 experts of 29, 39 workgroups: 34 against 35).
+// Else waves that share the long axis are faster: one row of an fp4 matrix 7168
+// to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 41 against 60,
+// 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 11 against 15.
+//
+// How many experts have rows is known on the device only; the host knows at most
+// how many can (no more than there are experts, or rows of the buffer). Where
+// that bound is too low for the wide kernel the split kernel runs, else the wide
+// kernel, which counts and takes 16 rows at a time itself if they are too few
+// (its four waves sharing the long axis). Padding makes that common. At A = 16 or
+// 128, one row each for 8 of 256 experts, 4096 to 512 in fp4: 8.8 us against 15.5
+// with 128 rows at a time (7.0 at A = 1, where the bound is 8); 4096 to 1024 in
+// fp8 14.1 against 18.4; 4 of 64 experts of 4 rows, 7168 to 512 in fp8, 11.0
+// against 27. Counting costs full buffers up to 2% (256 fp8 experts of 4 rows,
+// 1024 to 2048, 104 against 102).
+__host__ __device__ constexpr bool matvec_is_wide(int64_t experts, int64_t rows, int tiles) {
+  const int64_t units = experts * tiles;
+  return units >= kComputeUnits * 3 / 8 || (units >= kComputeUnits / 5 && rows > kTile * experts);
+}
+
+// 16 rows of a matrix for all rows of its expert, the workgroup's waves sharing the long axis.
+template <int WT, bool FP32>
+__device__ __forceinline__ void matvec_split_unit(const uint16_t *x, const void *w, const float *scales,
+                                                  const Segment &seg, int n0, int K, int N, void *y, float *red) {
+  const int r = lane_id() & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
+  const int steps = (K + kStep - 1) / kStep;
+  const Matrix m = matrix_of<WT>(w, scales, seg.e, N, K);
+  const int row[1] = {n0 + r < N ? n0 + r : -1};
+  for (int64_t p = 0; p < seg.count; p += kTile) {
+    const int rows = (int)(seg.count - p < kTile ? seg.count - p : kTile);
+    // rows beyond the group lie outside the descriptor
+    const __amdgpu_buffer_rsrc_t xb = buffer_of(x + (seg.begin + p) * K, (int64_t)rows * K * 2);
+    f32x4 acc[1] = {};
+    multiply<WT, 1>(m, row, xb, r < rows ? (uint32_t)r * (uint32_t)K * 2u : kOutside, steps * wave / waves,
+                    steps * (wave + 1) / waves, acc);
+    red_put<1>(red, wave, acc);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
+      const int c = i % kTile, q = i / kTile;
+      if (q < rows && n0 + c < N) {
+        const float v = red_sum<1>(red, waves, 0, q, c);
+        const int64_t at = (seg.begin + p + q) * (int64_t)N + n0 + c;
+        if constexpr (FP32) ((float *)y)[at] = v;
+        else ((uint16_t *)y)[at] = bf16_bits(v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Few tiles: the 4 to 16 waves of a workgroup share 16 rows' long axis.
+template <int WT, bool FP32>
+__global__ __launch_bounds__(1024) void ep_expert_matvec_split(
+    const uint16_t *__restrict__ x, const void *__restrict__ w, const float *__restrict__ scales,
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int E,
+    int64_t capacity, int K, int N, int64_t units, int tiles, void *__restrict__ y) {
+  extern __shared__ float red[];
+  int have_j = -1;
+  Segment seg{-1, 0, 0};
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * kTile;
+    if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
+    have_j = j;
+    if (seg.e < 0) return;  // no further expert has rows
+    matvec_split_unit<WT, FP32>(x, w, scales, seg, n0, K, N, y, red);
+  }
+}
+
+// Many tiles: a workgroup takes 128 rows of one expert's matrix, or where the experts with rows turn out
+// to be too few for that, 16 as above.
 template <int WT, bool FP32>
 __global__ __launch_bounds__(kThreads, 2) void ep_expert_matvec_wide(
     const uint16_t *__restrict__ x, const void *__restrict__ w, const float *__restrict__ scales,
@@ -514,8 +607,22 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_matvec_wide(
     int64_t capacity, int K, int N, int64_t units, int tiles, void *__restrict__ y) {
   __shared__ __attribute__((aligned(16))) char lds[wide_lds_bytes<WT, 2>()];
   __shared__ uint32_t tok_off[2 * kTile];
-  int have_j = -1;
-  Segment seg{-1, 0, 0};
+  int experts = 0;
+  int have_j = (int)(blockIdx.x / tiles);
+  Segment seg = find_segment<true>(have_j, counts, offsets, E, capacity, &experts);
+  if (counts != nullptr && !matvec_is_wide(experts, 0, tiles) &&
+      !matvec_is_wide(experts, rows_of_all(counts, offsets, E, capacity), tiles)) {
+    const int tiles16 = (N + kTile - 1) / kTile;
+    const int64_t units16 = (int64_t)experts * tiles16;
+    have_j = -1;
+    for (int64_t u = blockIdx.x; u < units16; u += gridDim.x) {
+      const int j = (int)(u / tiles16), n0 = (int)(u - (int64_t)j * tiles16) * kTile;
+      if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
+      have_j = j;
+      matvec_split_unit<WT, FP32>(x, w, scales, seg, n0, K, N, y, (float *)lds);
+    }
+    return;
+  }
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * kWideTiles * kTile * 4;
     if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
@@ -530,48 +637,6 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_matvec_wide(
       else
         matvec_wide_group<WT, 1, FP32>(m, x, seg.begin + p, rows, n0, N, y, lds, tok_off);
       p += rows;
-    }
-  }
-}
-
-// Few tiles: the 4 to 16 waves of a workgroup share 16 rows' long axis.
-template <int WT, bool FP32>
-__global__ __launch_bounds__(1024) void ep_expert_matvec_split(
-    const uint16_t *__restrict__ x, const void *__restrict__ w, const float *__restrict__ scales,
-    const int32_t *__restrict__ counts, const int32_t *__restrict__ offsets, int E,
-    int64_t capacity, int K, int N, int64_t units, int tiles, void *__restrict__ y) {
-  extern __shared__ float red[];
-  const int r = lane_id() & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
-  const int steps = (K + kStep - 1) / kStep;
-  int have_j = -1;
-  Segment seg{-1, 0, 0};
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int j = (int)(u / tiles), n0 = (int)(u - (int64_t)j * tiles) * kTile;
-    if (j != have_j) seg = find_segment(j, counts, offsets, E, capacity);
-    have_j = j;
-    if (seg.e < 0) return;  // no further expert has rows
-    const Matrix m = matrix_of<WT>(w, scales, seg.e, N, K);
-    const int row[1] = {n0 + r < N ? n0 + r : -1};
-    for (int64_t p = 0; p < seg.count; p += kTile) {
-      const int rows = (int)(seg.count - p < kTile ? seg.count - p : kTile);
-      // rows beyond the group lie outside the descriptor
-      const __amdgpu_buffer_rsrc_t xb = buffer_of(x + (seg.begin + p) * K, (int64_t)rows * K * 2);
-      f32x4 acc[1] = {};
-      multiply<WT, 1>(m, row, xb, r < rows ? (uint32_t)r * (uint32_t)K * 2u : kOutside, steps * wave / waves,
-                      steps * (wave + 1) / waves, acc);
-      red_put<1>(red, wave, acc);
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
-        const int c = i % kTile, q = i / kTile;
-        if (q < rows && n0 + c < N) {
-          const float v = red_sum<1>(red, waves, 0, q, c);
-          const int64_t at = (seg.begin + p + q) * (int64_t)N + n0 + c;
-          if constexpr (FP32) ((float *)y)[at] = v;
-          else ((uint16_t *)y)[at] = bf16_bits(v);
-        }
-      }
-      __syncthreads();
     }
   }
 }
@@ -1023,7 +1088,6 @@ __global__ __launch_bounds__(down_waves(RT, NG) * kWave) void ep_moe_down(
   }
 }
 
-constexpr int kComputeUnits = 256;
 constexpr int64_t kMaxBlocks = (1 << 22) - 1;  // of at most 1024 threads: within the grid limit of 2^32
 
 template <int WT>
@@ -1053,7 +1117,10 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
   const int tiles = (a.N + kRows - 1) / kRows;
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
   const int64_t units = experts * tiles;
-  const int64_t most = cap > 0 ? cap : kMaxBlocks;
+  // Four workgroups for every compute unit, which loop: experts without rows then cost no workgroup each
+  // (8 of 256 experts with a row, 2048 to 4096 in fp4 at A = 16: 12.7 us, 31 with a workgroup for every
+  // tile that may be; 64 experts of 16 rows, 2048 tiles that all are: 201 us either way).
+  const int64_t most = cap > 0 ? cap : 4 * kComputeUnits;
   const unsigned blocks = (unsigned)(units < most ? units : most);
   if (a.fp32)
     ep_expert_matvec_wide<WT, true><<<blocks, kThreads, 0, a.stream>>>(
@@ -1066,23 +1133,11 @@ int matvec_wide_launch(const ExpertMatvecArgs &a, int cap) {
   return launch_status();
 }
 
-// The wide kernel reads x once for 128 rows and walks the whole long axis: right
-// where its workgroups take most compute units (24 fp8 experts of 4 rows, 4096
-// to 1024, 192 workgroups: 20 against 48 us; one fp4 row to 14336, 112: 23
-// against 32; 12 experts of a row, 96: 17 against 19 in fp8, 21 against 20 in
-// bf16), or a fifth of them and the split kernel would read every matrix again
-// for each 16 of more rows (one bf16 expert of 64 rows, 7168 to 7168, 56
-// workgroups: 83 against 114; 3 experts of 29, 39 workgroups: 34 against 35).
-// Else waves that share the long axis are faster: one row of an fp4 matrix 7168
-// to 4096 (32 workgroups) 10 against 25 us, 40 rows of it in fp8 41 against 60,
-// 8 experts of a row, 4096 to 1024 in fp4 (64 workgroups) 11 against 15.
 template <int WT>
 int matvec_pick(const ExpertMatvecArgs &a, int cap) {
   const int64_t experts = a.counts == nullptr ? 1 : (a.E < a.capacity ? a.E : a.capacity);
-  const int64_t wide_tiles = (a.N + 4 * kWideTiles * kTile - 1) / (4 * kWideTiles * kTile);
-  const int64_t units = experts * wide_tiles;
-  const bool wide = units >= kComputeUnits * 3 / 8 || (units >= kComputeUnits / 5 && a.capacity > kTile * experts);
-  return wide ? matvec_wide_launch<WT>(a, cap) : matvec_split_launch<WT>(a, cap);
+  const int wide_tiles = (a.N + 4 * kWideTiles * kTile - 1) / (4 * kWideTiles * kTile);
+  return matvec_is_wide(experts, a.capacity, wide_tiles) ? matvec_wide_launch<WT>(a, cap) : matvec_split_launch<WT>(a, cap);
 }
 
 struct MoeWorkspace {
