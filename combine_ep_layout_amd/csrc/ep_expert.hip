@@ -1198,11 +1198,16 @@ int moe_down_launch(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap, int 
 // 27 us with 4 entries an expert, 28 against 37 with 16), else 16 and the long
 // axis shared (8 fp4 experts of one token, 176 workgroups: 16 against 18 us; 4
 // fp8 experts of 32 entries, 64: 29 against 38; one bf16 expert, 32: 18 against
-// 54).
+// 54). Counted by the experts that the entries could have, not by those that they
+// have, which only the device knows: counting there made a few tokens' layer (about
+// 18 of 32 fp8 experts active) 37 us instead of 26 and the hot cases 15% slower to
+// 20% faster.
 // Second launch: two groups of eight tokens a pass where experts have more than
 // eight entries on the average (64 fp4 experts, 16 entries each: 255 against
 // 266 us; 16 fp8 experts of 64: 191 against 237), else one (197 active fp4
-// experts, 5 entries each: 473 against 528).
+// experts, 5 entries each: 473 against 528). The average is over all experts too: entries
+// that all go to 8 of 256 experts (64 tokens, top-8, fp8, 4096 / 512) take 68 us, 62 in a call
+// with these 8 experts alone, 64 entries of 4 of 64 bf16 experts (1024 / 512) 19 against 16.
 template <int WT>
 int moe_pick(const MoeLayerArgs &a, const MoeWorkspace &ws, int cap) {
   const int n = a.T * a.K;
