@@ -20,10 +20,12 @@
 // on their way into registers, one in the other half of LDS, and loads and LDS
 // stores are issued between the matrix instructions of a step (all at its
 // start: 11% slower).
-// Measured on MI355X: 64 experts of 128 e4m3 rows 965 us (4.0 TB/s), with
-// scales that are no powers of two (three products for every one, below) 2355;
-// 8 experts of 2048 rows, 4096 by 2048, added to an fp32 gradient, 308 us in
-// bf16 (890 TFLOP/s), 315 in e4m3 and 927 with scales of any kind.
+// Measured on MI355X: 64 experts of 128 e4m3 rows 1080 us (3.6 TB/s), with
+// scales that are no powers of two (three products for every one, below) 2340;
+// 8 experts of 2048 rows, 4096 by 2048, added to an fp32 gradient, 310 us in
+// bf16 (885 TFLOP/s), 312 in e4m3 and 928 with scales of any kind. No kernel
+// spills: a register that comes back from memory waits for every load and store
+// of its wave (64 experts: 1153 us with one).
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -60,7 +62,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
 }
 
 // The same in every lane, said so: a descriptor that the compiler takes for a lane's own costs a loop
-// around every access and registers (8 experts of 2048 bf16 rows 331 us against 308, and spills).
+// around every access and registers (8 experts of 2048 bf16 rows 334 us against 310, and spills).
 __device__ __forceinline__ const char *uniform(const char *p) {
   const uint64_t v = (uint64_t)p;
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
@@ -90,7 +92,7 @@ __device__ __forceinline__ bf16x8 column(const char *upper, const char *lower) {
 // (bf16's least step) is lost. Rounding x to bf16 instead would put the
 // gradient of 128 rows with scales in [0.01, 1] off by 1.7e-3 where the sum in
 // binary32 is off by 2e-7. What the scales are is found on the way: a tile is
-// begun with one product, and begun again with three where a value was rounded.
+// begun with one product, and begun again with three where a scale asks for it.
 __device__ __forceinline__ void three_parts(float p, uint32_t (&part)[3]) {  // in the upper halves
 #pragma clang fp contract(off)  // p is one rounded value: fused with its product, the parts could come from two
   part[0] = __float_as_uint(p);
@@ -116,7 +118,7 @@ struct Stage {
   u32x4 v[2][kPieces];
   float scale[2][kPiecesX];
   bool scaled;
-  bool rounded = false;  // a value of x in the pieces stored so far was (the same in all lanes)
+  bool indirect = false;  // this lane has stored a piece whose scale is not for the direct conversion
 
   static __device__ __forceinline__ int row_y(int i) { return (threadIdx.x + i * kThreads) / (kTileN / 8); }
   static __device__ __forceinline__ int col_y(int i) { return (threadIdx.x + i * kThreads) % (kTileN / 8) * 8; }
@@ -164,35 +166,19 @@ struct Stage {
     if (i < 2) {
       *(u32x4 *)(ly + row_y(i) * kStrideY + col_y(i) * 2) = v[set][i];
     } else if constexpr (FP8) {
-      // One instruction converts two values where every lane of the wave can: rows behind the end
-      // and groups of zeros (codes 0 and a finite scale) count as scaled by 1. Other scales multiply
-      // in binary32 and round; values that this changes are noted, but for those below 2^-126, whose
-      // bits bf16 cannot hold in any number of parts.
+      // One instruction converts two values: powers of two, and rows behind the end and groups of
+      // zeros (codes 0 and a finite scale), which count as scaled by 1. A step with any other scale
+      // is noted; its tile is done again.
       const u32x4 c = v[set][i];
       float s = scaled ? scale[set][i - 2] : 1.0f;
       if ((c[0] | c[1] | c[2] | c[3]) == 0 && (__float_as_uint(s) & 0x7F800000u) != 0x7F800000u) s = 1.0f;
       const uint32_t bits = __float_as_uint(s);
-      const bool direct = (bits & 0x807FFFFFu) == 0 && bits >= 0x1F800000u && bits <= 0x5F800000u;
+      indirect |= (bits & 0x807FFFFFu) != 0 || bits < 0x1F800000u || bits > 0x5F800000u;
       u32x4 w[2];
-      if (ballot(!direct) == 0) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          w[d >> 1][(d & 1) * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, false));
-          w[d >> 1][(d & 1) * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, true));
-        }
-      } else {
-        uint32_t lost = 0;
-        const auto two = [&](f32x2 q) {
-          const uint32_t lo = __float_as_uint(q[0] * s), hi = __float_as_uint(q[1] * s);
-          lost |= ((lo & 0x7F800000u) != 0 ? lo & 0xFFFFu : 0u) | ((hi & 0x7F800000u) != 0 ? hi & 0xFFFFu : 0u);
-          return pack(__uint_as_float(lo), __uint_as_float(hi));
-        };
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          w[d >> 1][(d & 1) * 2] = two(__builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], false));
-          w[d >> 1][(d & 1) * 2 + 1] = two(__builtin_amdgcn_cvt_pk_f32_fp8((int)c[d], true));
-        }
-        rounded = rounded || ballot(lost != 0) != 0;
+      for (int d = 0; d < 4; ++d) {
+        w[d >> 1][(d & 1) * 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, false));
+        w[d >> 1][(d & 1) * 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[d], s, true));
       }
       put_x(lx, row_x(i - 2), col_x(i - 2), w[0]);
       put_x(lx, row_x(i - 2), col_x(i - 2) + 8, w[1]);
@@ -247,12 +233,12 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
   const int row = g * 4 + (r16 >> 2);
   const int at_y = row * kStrideY + wn * 2 + (r16 & 3) * 8;
   const int at_x = kRows * kStrideY + row * kStrideX + wh / 2 + (r16 & 1) * 2 * kPlaneX + (r16 >> 1 & 1) * 8;
-  // Whether a wave has rounded a value of x in the first step, and in a later one: two sets in turn, so
-  // that one is cleared while no wave can still read or write it.
-  __shared__ int rounded[2][2];
+  // Whether some scale was not for the direct conversion, in the first step and in a later one: two sets
+  // in turn, so that one is cleared while no wave can still read or write it.
+  __shared__ int indirect[2][2];
   int turn = 0;
   if constexpr (FP8) {
-    if (threadIdx.x < 4) rounded[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+    if (threadIdx.x < 4) indirect[threadIdx.x >> 1][threadIdx.x & 1] = 0;
     __syncthreads();
   }
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -298,17 +284,17 @@ __global__ __launch_bounds__(kThreads, 2) void ep_expert_wgrad_tiles(
         stage.store(0, i, lds, lds + kRows * kStrideY);
         stage.load(0, i);
       }
-      int *const seen = rounded[turn];
+      int *const seen = indirect[turn];
       if constexpr (FP8)
-        if (stage.rounded) seen[0] = 1;
+        if (stage.indirect) seen[0] = 1;
       __syncthreads();
       if constexpr (FP8) {
         turn ^= 1;  // every wave has left the last tile: its set is free
-        if (threadIdx.x < 2) rounded[turn][threadIdx.x] = 0;
+        if (threadIdx.x < 2) indirect[turn][threadIdx.x] = 0;
       }
       const auto step = [&](auto set, auto first) {  // products of the step in lds[set]
         if constexpr (FP8)
-          if (stage.rounded) seen[1] = 1;  // in the steps stored so far; the last one stores rows behind the end
+          if (stage.indirect) seen[1] = 1;  // in the steps stored so far; the last one stores rows behind the end
         aim();
         const char *sy = lds + set * kStepBytes + at_y, *sx = lds + set * kStepBytes + at_x;
         char *to = lds + (set ^ 1) * kStepBytes;

@@ -541,9 +541,10 @@ int ep_swiglu_backward(const void *dh, const void *checkpoint, const float *chec
  * with x kept in bf16 or in 8 bits (rows as dispatch moves them, or a
  * checkpoint): x[r] = code * x_scales[r], rounded to binary32 (and to a
  * multiple of 2^-133, which matters below 2^-110). Summed in binary32, rounded
- * once. Scales that are powers of two, such as ep_swiglu's, take one pass of
- * the matrix cores, others three (64 experts of 128 rows 965 and 2355 us on
- * MI355X). An expert without rows gets previous[e], or zeros.
+ * once. Scales that are powers of two from 2^-64 to 2^64, as ep_swiglu's are
+ * but for tiny rows, take one pass of the matrix cores, others three (64
+ * experts of 128 rows 1080 and 2340 us on MI355X). An expert without rows gets
+ * previous[e], or zeros.
  *
  *   dy          bf16 [capacity_rows, out_features]
  *   x           bf16 or e4m3 (x_dtype) [capacity_rows, in_features]
