@@ -22,9 +22,9 @@
 // plain loads (non-temporal ones lose 5 to 30%: 53 against 41 us in the second
 // launch of one token).
 // Measured on MI355X: a bf16 layer of one token, top-8, hidden 7168,
-// intermediate 2048 (705 MB of weights) 123 us, 5.7 TB/s; 128 tokens over 197
-// active fp4 experts of 256 (4.6 GB) 1000 to 1046 us, 4.5 TB/s; fp4 products of 1024
-// rows over 64 experts, 7168 to 4096 (1.0 GB) 207 us, 4.9 TB/s.
+// intermediate 2048 (705 MB of weights) 122 us, 5.8 TB/s; 128 tokens over 197
+// active fp4 experts of 256 (4.6 GB) 1015 to 1050 us, 4.5 TB/s; fp4 products of 1024
+// rows over 64 experts, 7168 to 4096 (1.0 GB) 212 to 216 us, 4.8 TB/s.
 #include <type_traits>
 
 #include "ep_device.hpp"

@@ -14,6 +14,10 @@
 //   d_gate = dh * up * s * (1 + gate * (1 - s)),  d_up = dh * gate * s.
 // All arithmetic in binary32, results rounded once.
 //
+// Measured on MI355X, 32768 rows of 2048 in bf16 with the checkpoint: 101 us
+// forward, 126 backward (87 and 113 in the kernel, 5.4 TB/s); the pairs below
+// compare two forms of one kernel as they stood when the choice was made.
+//
 // What bounds both is HBM: 6 to 8 bytes per value pair of bf16 rows and the
 // checkpoint's 2.06. So: one pass, a lane takes eight channels (16-byte loads
 // of gate and up), 16 lanes hold a scale group and find its maximum with four

@@ -467,7 +467,8 @@ size_t ep_moe_layer_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t in
  *   workspace     >= ep_moe_layer_workspace_bytes, 16-byte aligned
  * hidden and intermediate are multiples of 8 (128 for scaled weights).
  * Errors: EP_EUNSUPPORTED for num_tokens * topk > EP_MOE_MAX_ENTRIES (use
- * layout, dispatch, ep_expert_matvec or a grouped product, and combine);
+ * layout, dispatch, ep_expert_matvec or the caller's own grouped product, and
+ * combine);
  * EP_EINVAL otherwise.
  */
 int ep_moe_layer(const void *x, const int32_t *topk_idx, const float *topk_weights,
@@ -570,8 +571,8 @@ int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const 
  *
  * Caps every kernel this library launches on `stream` (a hipStream_t; NULL
  * is the null stream) at max_workgroups workgroups, each sized to keep one
- * compute unit busy (1024 threads; 512 for combine), whose waves loop over
- * the work; the other compute units stay free for kernels on other streams.
+ * compute unit busy (1024 threads; 512 for combine; the experts' operators
+ * keep their own 256 to 1024), whose waves loop over the work; the other compute units stay free for kernels on other streams.
  * Results are identical with and without a cap. max_workgroups = 0 removes
  * the cap (the default: grids cover all work with 256-thread workgroups);
  * values above the current device's compute-unit count are clamped to it.
