@@ -303,7 +303,7 @@ def _plain(s, case):
         v = gate / (1 + torch.exp(-gate)) * up
     top = v.abs().amax(1, keepdim=True).clamp(min=LEAST)
     # the product of two 32-bit numbers is exact in 64, so that a value between two codes goes to the even one
-    code = torch.round(v.double() * (127 / top).double())
+    code = torch.round(v.double() * (torch.full_like(top, 127.0) / top).double())
     codes = torch.where(live[:, None], code.to(torch.int8), s["codes"])
     scales = torch.where(live[:, None], (top / 127).expand(-1, case["copies"]), s["scales"])
     return {"codes": codes.to(torch.bfloat16) if op == "swiglu_quantize" else codes, "scales": scales}
@@ -452,9 +452,9 @@ def exact(case, seed):
         v = gate * torch.sigmoid(gate) * up
     top = v.abs().amax(1, keepdim=True).clamp(min=LEAST)
     if op == "quantize_rows":  # by the factor 127 / top in 32 bits, as the operator is defined
-        code = torch.round(v * (127 / top).float().double()).to(torch.int8)
+        code = torch.round(v * (torch.full_like(top, 127.0) / top).float().double()).to(torch.int8)
     else:
-        code = torch.round(v * (127 / top))
+        code = torch.round(v * 127 / top)
     codes = torch.zeros(s["cap"], case["width"], dtype=code.dtype, device="cuda")
     codes[at] = code
     scales = torch.zeros(s["cap"], case["copies"], dtype=torch.float64, device="cuda")
