@@ -27,6 +27,11 @@ EP_FP32 = 1
 EP_FP8_E4M3 = 2
 EP_FP4X2 = 3
 
+EP_SOFTMAX = 0
+EP_SIGMOID = 1
+
+EP_MAX_SEQUENCES = 65536
+EP_MAX_QUANTIZED_WIDTH = 131056
 EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 64
 EP_LAYOUT_SCRATCH_BYTES = 8 << 20
@@ -38,7 +43,9 @@ SYMBOLS = ("ep_layout_workspace_bytes", "ep_layout", "ep_dispatch", "ep_layout_d
            "ep_zero_padding", "ep_set_workgroup_limit",
            "ep_get_workgroup_limit", "ep_last_error", "ep_supported", "ep_layout_noalloc",
            "ep_layout_dispatch_workspace_bytes", "ep_moe_layer", "ep_moe_layer_workspace_bytes",
-           "ep_expert_matvec", "ep_swiglu", "ep_swiglu_backward", "ep_expert_wgrad")
+           "ep_expert_matvec", "ep_swiglu", "ep_swiglu_backward", "ep_expert_wgrad",
+           "ep_router", "ep_router_workspace_bytes", "ep_router_backward", "ep_quantize_rows",
+           "ep_swiglu_quantize", "ep_quantized_matmul")
 
 
 class EpError(RuntimeError):
@@ -55,6 +62,7 @@ _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 def lib(path: str = None) -> ctypes.CDLL:
@@ -116,6 +124,19 @@ def lib(path: str = None) -> ctypes.CDLL:
     L.ep_swiglu_backward.restype = ctypes.c_int
     L.ep_expert_wgrad.argtypes = [_vp] * 5 + [_i32, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp]
     L.ep_expert_wgrad.restype = ctypes.c_int
+    L.ep_router_workspace_bytes.argtypes = [_i32, _i32, _i32]
+    L.ep_router_workspace_bytes.restype = _sz
+    L.ep_router.argtypes = [_vp] * 4 + [_i32] * 7 + [_f32, _i32] + [_vp] * 7 + [_sz, _vp]
+    L.ep_router.restype = ctypes.c_int
+    L.ep_router_backward.argtypes = [_vp] * 8 + [_i32] * 7 + [_f32, _vp, _vp]
+    L.ep_router_backward.restype = ctypes.c_int
+    L.ep_quantize_rows.argtypes = [_vp] * 3 + [_i32, _i64, _i32, _i32, _vp, _vp, _i32, _vp]
+    L.ep_quantize_rows.restype = ctypes.c_int
+    L.ep_swiglu_quantize.argtypes = [_vp] * 3 + [_i32, _i64, _i32, _i32, _vp, _vp, _i32, _vp]
+    L.ep_swiglu_quantize.restype = ctypes.c_int
+    L.ep_quantized_matmul.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp,
+                                      _i32, _vp]
+    L.ep_quantized_matmul.restype = ctypes.c_int
     if path is None:
         _LIB = L
     return L
@@ -305,3 +326,47 @@ def ep_expert_wgrad(dy, x, x_scales, counts, offsets, num_experts, capacity_rows
     _check(lib().ep_expert_wgrad(_p(dy), _p(x), _p(x_scales), _p(counts), _p(offsets), num_experts,
                                  capacity_rows, out_features, in_features, x_dtype, _p(previous),
                                  _p(dw), dw_dtype, _s(stream)))
+
+
+def ep_router_workspace_bytes(num_tokens: int, num_experts: int, num_sequences: int = 1) -> int:
+    return int(lib().ep_router_workspace_bytes(num_tokens, num_experts, num_sequences))
+
+
+def ep_router(logits, select_bias, token_mask, seq_offsets, num_tokens, num_experts, topk,
+              num_sequences, dtype, scoring, normalize, scale, given, topk_idx, topk_weights,
+              counts=None, seq_tokens=None, balance_loss=None, z_loss=None, workspace=None,
+              workspace_bytes=0, stream=None):
+    _check(lib().ep_router(_p(logits), _p(select_bias), _p(token_mask), _p(seq_offsets), num_tokens,
+                           num_experts, topk, num_sequences, dtype, scoring, normalize, scale, given,
+                           _p(topk_idx), _p(topk_weights), _p(counts), _p(seq_tokens),
+                           _p(balance_loss), _p(z_loss), _p(workspace), workspace_bytes,
+                           _s(stream)))
+
+
+def ep_router_backward(logits, topk_idx, seq_offsets, counts, seq_tokens, d_topk_weights,
+                       d_balance_loss, d_z_loss, num_tokens, num_experts, topk, num_sequences, dtype,
+                       scoring, normalize, scale, d_logits, stream=None):
+    _check(lib().ep_router_backward(_p(logits), _p(topk_idx), _p(seq_offsets), _p(counts),
+                                    _p(seq_tokens), _p(d_topk_weights), _p(d_balance_loss),
+                                    _p(d_z_loss), num_tokens, num_experts, topk, num_sequences,
+                                    dtype, scoring, normalize, scale, _p(d_logits), _s(stream)))
+
+
+def ep_quantize_rows(x, counts, offsets, num_experts, capacity_rows, width, dtype, codes, scales,
+                     scale_cols=1, stream=None):
+    _check(lib().ep_quantize_rows(_p(x), _p(counts), _p(offsets), num_experts, capacity_rows, width,
+                                  dtype, _p(codes), _p(scales), scale_cols, _s(stream)))
+
+
+def ep_swiglu_quantize(gate_up, counts, offsets, num_experts, capacity_rows, intermediate, dtype,
+                       codes, scales, scale_cols=1, stream=None):
+    _check(lib().ep_swiglu_quantize(_p(gate_up), _p(counts), _p(offsets), num_experts, capacity_rows,
+                                    intermediate, dtype, _p(codes), _p(scales), scale_cols,
+                                    _s(stream)))
+
+
+def ep_quantized_matmul(x, x_scales, x_scale_cols, w, w_scales, counts, offsets, num_experts,
+                        capacity_rows, in_features, out_features, y, y_dtype, stream=None):
+    _check(lib().ep_quantized_matmul(_p(x), _p(x_scales), x_scale_cols, _p(w), _p(w_scales),
+                                     _p(counts), _p(offsets), num_experts, capacity_rows,
+                                     in_features, out_features, _p(y), y_dtype, _s(stream)))

@@ -26,7 +26,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libep_mi355x.so")
 
 SOURCES = ["ep_capi.cpp", "ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_padding.hip",
-           "ep_compact.hip", "ep_expert.hip", "ep_swiglu.hip", "ep_wgrad.hip"]
+           "ep_compact.hip", "ep_expert.hip", "ep_swiglu.hip", "ep_wgrad.hip", "ep_router.hip",
+           "ep_quantize.hip", "ep_quantized.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -900,3 +900,221 @@ int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const 
 }
 
 }  // extern "C"
+
+// ------------------------------------------- the router's and the 8-bit integer operators
+
+namespace {
+
+int check_router(const char *what, int32_t T, int32_t E, int32_t K, int32_t S, int32_t dtype,
+                 int32_t scoring, float scale, const int32_t *seq_offsets, const int32_t *counts,
+                 const int32_t *seq_tokens) {
+  if (int rc = check_topk(what, T, K)) return rc;
+  if (int rc = check_experts(what, E)) return rc;
+  if (dtype != EP_BF16 && dtype != EP_FP32)
+    return fail(EP_EINVAL, "%s: logits are bf16 or fp32 (got dtype %d)", what, dtype);
+  if (scoring != EP_SOFTMAX && scoring != EP_SIGMOID)
+    return fail(EP_EINVAL, "%s: unknown scoring %d", what, scoring);
+  if (!(scale - scale == 0.f))
+    return fail(EP_EINVAL, "%s: scale must be finite", what);
+  if (S < 1 || S > EP_MAX_SEQUENCES)
+    return fail(EP_EINVAL, "%s: num_sequences must be in 1..%d (got %d)", what, EP_MAX_SEQUENCES, S);
+  if (seq_offsets == nullptr && S != 1)
+    return fail(EP_EINVAL, "%s: %d sequences need seq_offsets", what, S);
+  if ((counts == nullptr) != (seq_tokens == nullptr))
+    return fail(EP_EINVAL, "%s: counts and seq_tokens go together", what);
+  if (!aligned(seq_offsets, 4) || !aligned(counts, 4) || !aligned(seq_tokens, 4))
+    return fail(EP_EINVAL, "%s: misaligned pointer (int32 arrays need 4 bytes)", what);
+  return EP_OK;
+}
+
+// Rows of int8 codes, `width` values each, and their scales.
+int check_codes(const char *what, int32_t width, int32_t dtype, const void *x, const void *codes,
+                const float *scales, int32_t scale_cols, int64_t capacity_rows, int factor) {
+  if (int rc = check_row_dtype(what, dtype)) return rc;
+  if (width < 16 || width % 16 != 0 || width > (1 << 24))
+    return fail(EP_EINVAL, "%s: rows must be a positive multiple of 16 values up to 2^24 (got %d)",
+                what, width);
+  if (scale_cols < 1 || scale_cols > (1 << 20))
+    return fail(EP_EINVAL, "%s: scale_cols must be in 1..2^20 (got %d)", what, scale_cols);
+  if (capacity_rows > 0 && (!x || !codes || !scales))
+    return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+  const int64_t bytes = capacity_rows * width;
+  if (overlap(codes, bytes, x, bytes * factor * (dtype == EP_FP32 ? 4 : 2)))
+    return fail(EP_EINVAL, "%s: the codes must not overlap their input", what);
+  return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ep_router_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t num_sequences) {
+  try {
+    if (num_tokens < 0 || num_experts < 1 || num_experts > EP_MAX_EXPERTS || num_sequences < 1 ||
+        num_sequences > EP_MAX_SEQUENCES)
+      return 0;
+    return ep::router_workspace(num_tokens, num_experts, num_sequences);
+  } catch (...) {
+    return 0;
+  }
+}
+
+int ep_router(const void *logits, const float *select_bias, const uint8_t *token_mask,
+              const int32_t *seq_offsets, int32_t num_tokens, int32_t num_experts, int32_t topk,
+              int32_t num_sequences, int32_t dtype, int32_t scoring, int32_t normalize, float scale,
+              int32_t given, int32_t *topk_idx, float *topk_weights, int32_t *counts,
+              int32_t *seq_tokens, float *balance_loss, float *z_loss, void *workspace,
+              size_t workspace_bytes, void *stream) {
+  try {
+    const char *what = "ep_router";
+    discard_stale_error();
+    if (int rc = check_router(what, num_tokens, num_experts, topk, num_sequences, dtype, scoring,
+                              scale, seq_offsets, counts, seq_tokens))
+      return rc;
+    if (!given && topk > num_experts)
+      return fail(EP_EINVAL, "%s: top-%d of %d experts", what, topk, num_experts);
+    if (given && (select_bias != nullptr || token_mask != nullptr))
+      return fail(EP_EINVAL, "%s: given ids take no select_bias and no token_mask", what);
+    if (counts == nullptr && (balance_loss != nullptr || z_loss != nullptr))
+      return fail(EP_EINVAL, "%s: the losses need counts and seq_tokens", what);
+    if (z_loss != nullptr && scoring != EP_SOFTMAX)
+      return fail(EP_EINVAL, "%s: the z loss is of softmax scores", what);
+    if (num_tokens > 0 && (!logits || !topk_idx))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(logits, 16) || !aligned(workspace, 16) || !aligned(select_bias, 4) ||
+        !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(balance_loss, 4) ||
+        !aligned(z_loss, 4))
+      return fail(EP_EINVAL, "%s: misaligned pointer (logits and the workspace need 16 bytes)", what);
+    if (counts != nullptr) {
+      const size_t need = ep::router_workspace(num_tokens, num_experts, num_sequences);
+      if (!workspace || workspace_bytes < need)
+        return fail(EP_EINVAL, "%s: workspace of %zu bytes needed (got %zu)", what, need,
+                    workspace ? workspace_bytes : (size_t)0);
+    }
+    ep::RouterArgs a{logits, select_bias, token_mask, seq_offsets, num_tokens, num_experts, topk,
+                     num_sequences, dtype == EP_FP32, scoring == EP_SIGMOID, normalize != 0,
+                     given != 0, scale, topk_idx, topk_weights, counts, seq_tokens, balance_loss,
+                     z_loss, workspace, (hipStream_t)stream};
+    return from_launch(ep::launch_router(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_router: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_router: unknown exception");
+  }
+}
+
+int ep_router_backward(const void *logits, const int32_t *topk_idx, const int32_t *seq_offsets,
+                       const int32_t *counts, const int32_t *seq_tokens,
+                       const float *d_topk_weights, const float *d_balance_loss,
+                       const float *d_z_loss, int32_t num_tokens, int32_t num_experts,
+                       int32_t topk, int32_t num_sequences, int32_t dtype, int32_t scoring,
+                       int32_t normalize, float scale, void *d_logits, void *stream) {
+  try {
+    const char *what = "ep_router_backward";
+    discard_stale_error();
+    if (int rc = check_router(what, num_tokens, num_experts, topk, num_sequences, dtype, scoring,
+                              scale, seq_offsets, counts, seq_tokens))
+      return rc;
+    if (counts == nullptr && (d_balance_loss != nullptr || d_z_loss != nullptr))
+      return fail(EP_EINVAL, "%s: the losses' gradients need counts and seq_tokens", what);
+    if (d_z_loss != nullptr && scoring != EP_SOFTMAX)
+      return fail(EP_EINVAL, "%s: the z loss is of softmax scores", what);
+    if (num_tokens > 0 && (!logits || !topk_idx || !d_logits))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(logits, 16) || !aligned(d_logits, 16) || !aligned(topk_idx, 4) ||
+        !aligned(d_topk_weights, 4) || !aligned(d_balance_loss, 4) || !aligned(d_z_loss, 4))
+      return fail(EP_EINVAL, "%s: misaligned pointer (logits need 16 bytes)", what);
+    const int64_t bytes = (int64_t)num_tokens * num_experts * (dtype == EP_FP32 ? 4 : 2);
+    if (overlap(d_logits, bytes, logits, bytes))
+      return fail(EP_EINVAL, "%s: d_logits must not overlap logits", what);
+    ep::RouterBackwardArgs a{logits, topk_idx, seq_offsets, counts, seq_tokens, d_topk_weights,
+                             d_balance_loss, d_z_loss, num_tokens, num_experts, topk, num_sequences,
+                             dtype == EP_FP32, scoring == EP_SIGMOID, normalize != 0, scale,
+                             d_logits, (hipStream_t)stream};
+    return from_launch(ep::launch_router_backward(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_router_backward: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_router_backward: unknown exception");
+  }
+}
+
+int ep_quantize_rows(const void *x, const int32_t *counts, const int32_t *offsets,
+                     int32_t num_experts, int64_t capacity_rows, int32_t width, int32_t dtype,
+                     void *codes, float *scales, int32_t scale_cols, void *stream) {
+  try {
+    const char *what = "ep_quantize_rows";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_codes(what, width, dtype, x, codes, scales, scale_cols, capacity_rows, 1))
+      return rc;
+    ep::QuantizeArgs a{x, counts, offsets, num_experts, capacity_rows, width, dtype == EP_FP32,
+                       false, codes, scales, scale_cols, (hipStream_t)stream};
+    return from_launch(ep::launch_quantize(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_quantize_rows: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_quantize_rows: unknown exception");
+  }
+}
+
+int ep_swiglu_quantize(const void *gate_up, const int32_t *counts, const int32_t *offsets,
+                       int32_t num_experts, int64_t capacity_rows, int32_t intermediate,
+                       int32_t dtype, void *codes, float *scales, int32_t scale_cols,
+                       void *stream) {
+  try {
+    const char *what = "ep_swiglu_quantize";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_codes(what, intermediate, dtype, gate_up, codes, scales, scale_cols,
+                             capacity_rows, 2))
+      return rc;
+    ep::QuantizeArgs a{gate_up, counts, offsets, num_experts, capacity_rows, intermediate,
+                       dtype == EP_FP32, true, codes, scales, scale_cols, (hipStream_t)stream};
+    return from_launch(ep::launch_quantize(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_swiglu_quantize: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_swiglu_quantize: unknown exception");
+  }
+}
+
+int ep_quantized_matmul(const void *x, const float *x_scales, int32_t x_scale_cols, const void *w,
+                        const float *w_scales, const int32_t *counts, const int32_t *offsets,
+                        int32_t num_experts, int64_t capacity_rows, int32_t in_features,
+                        int32_t out_features, void *y, int32_t y_dtype, void *stream) {
+  try {
+    const char *what = "ep_quantized_matmul";
+    discard_stale_error();
+    if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
+    if (int rc = check_row_dtype(what, y_dtype)) return rc;
+    if (in_features < 16 || in_features % 16 != 0 || in_features > EP_MAX_QUANTIZED_WIDTH)
+      return fail(EP_EINVAL, "%s: in_features must be a positive multiple of 16 up to %d (got %d)",
+                  what, EP_MAX_QUANTIZED_WIDTH, in_features);
+    if (out_features < 8 || out_features % 8 != 0 || out_features > (1 << 24))
+      return fail(EP_EINVAL, "%s: out_features must be a positive multiple of 8 up to 2^24 (got %d)",
+                  what, out_features);
+    if ((int64_t)in_features * out_features > INT32_MAX)
+      return fail(EP_EINVAL, "%s: one expert's w has %lld bytes, 2^31 or more", what,
+                  (long long)in_features * out_features);
+    if (x_scale_cols < 1 || x_scale_cols > (1 << 20))
+      return fail(EP_EINVAL, "%s: x_scale_cols must be in 1..2^20 (got %d)", what, x_scale_cols);
+    if (!w || !w_scales || (capacity_rows > 0 && (!x || !x_scales || !y)))
+      return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(x_scales, 4) ||
+        !aligned(w_scales, 4))
+      return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    ep::QuantizedMatmulArgs a{x, x_scales, x_scale_cols, w, w_scales, counts, offsets, num_experts,
+                              capacity_rows, in_features, out_features, y, y_dtype == EP_FP32,
+                              (hipStream_t)stream};
+    return from_launch(ep::launch_quantized_matmul(a), what);
+  } catch (const std::exception &e) {
+    return fail(EP_EHIP, "ep_quantized_matmul: %s", e.what());
+  } catch (...) {
+    return fail(EP_EHIP, "ep_quantized_matmul: unknown exception");
+  }
+}
+
+}  // extern "C"

@@ -168,6 +168,61 @@ struct ExpertWgradArgs {
   hipStream_t stream;
 };
 
+struct RouterArgs {
+  const void *logits;
+  const float *bias;        // NULL: none
+  const uint8_t *mask;      // NULL: every token takes part
+  const int32_t *seq;       // NULL: one sequence of all tokens
+  int T, E, K, S;
+  bool fp32, sigmoid, normalize, given;
+  float scale;
+  int32_t *idx;
+  float *weights;           // NULL: not written
+  int32_t *counts, *seq_tokens;  // NULL: no statistics
+  float *balance, *z;       // NULL: not written
+  void *workspace;
+  hipStream_t stream;
+};
+
+struct RouterBackwardArgs {
+  const void *logits;
+  const int32_t *idx, *seq, *counts, *seq_tokens;
+  const float *d_weights, *d_balance, *d_z;  // each may be NULL
+  int T, E, K, S;
+  bool fp32, sigmoid, normalize;
+  float scale;
+  void *d_logits;
+  hipStream_t stream;
+};
+
+struct QuantizeArgs {
+  const void *x;  // rows of `width` values, or of [gate | up], 2 * width
+  const int32_t *counts, *offsets;  // both NULL: every row of the buffer
+  int E;
+  int64_t capacity;
+  int width;
+  bool fp32, gated;
+  void *codes;
+  float *scales;
+  int scale_cols;
+  hipStream_t stream;
+};
+
+struct QuantizedMatmulArgs {
+  const void *x;
+  const float *x_scales;
+  int x_scale_cols;
+  const void *w;
+  const float *w_scales;
+  const int32_t *counts, *offsets;  // both NULL: one expert, every row of the buffer
+  int E;
+  int64_t capacity;
+  int K, N;  // values per row of x, values per row of y
+  void *y;
+  bool fp32;  // rows of y are binary32 (else bf16)
+  hipStream_t stream;
+};
+
 // Launch geometry. By default a grid covers every unit of work with
 // 256-thread workgroups, so the hardware spreads it over all compute units.
 // A stream may carry a workgroup cap (ep_set_workgroup_limit): every kernel
@@ -277,6 +332,11 @@ int launch_expert_matvec(const ExpertMatvecArgs &a);
 int launch_swiglu(const SwigluArgs &a);
 int launch_swiglu_backward(const SwigluBackwardArgs &a);
 int launch_expert_wgrad(const ExpertWgradArgs &a);
+int launch_router(const RouterArgs &a);
+size_t router_workspace(int T, int E, int S);
+int launch_router_backward(const RouterBackwardArgs &a);
+int launch_quantize(const QuantizeArgs &a);
+int launch_quantized_matmul(const QuantizedMatmulArgs &a);
 
 bool has_layout(int K);
 bool has_dispatch(int H, int K, int dtype);

@@ -14,8 +14,12 @@
  *
  * between them, the experts' own part: ep_moe_layer (a whole layer for a few
  * tokens), ep_expert_matvec (products with bf16, 8-bit or 4-bit weights),
- * ep_swiglu / ep_swiglu_backward (the activation, with an 8-bit checkpoint)
- * and ep_expert_wgrad (the weight gradient),
+ * ep_swiglu / ep_swiglu_backward (the activation, with an 8-bit checkpoint),
+ * ep_expert_wgrad (the weight gradient), and the same path in 8-bit integers:
+ * ep_quantize_rows, ep_swiglu_quantize and ep_quantized_matmul,
+ *
+ * before them: ep_router (a router's logits -> topk_idx, topk_weights,
+ * per-expert counts, balance and z loss) and ep_router_backward,
  *
  * and around them: ep_layout_dispatch (layout + dispatch in one launch for a
  * one-tile batch), the non-expand mode (ep_dispatch_compact,
@@ -78,6 +82,17 @@ extern "C" {
 #define EP_FP32 1
 #define EP_FP8_E4M3 2
 #define EP_FP4X2 3
+
+/* Scores of ep_router. */
+#define EP_SOFTMAX 0
+#define EP_SIGMOID 1
+
+/* Largest num_sequences of ep_router. */
+#define EP_MAX_SEQUENCES 65536
+
+/* Largest in_features of ep_quantized_matmul: a sum of that many products of two 8-bit
+ * integers is below 2^31. */
+#define EP_MAX_QUANTIZED_WIDTH 131056
 
 /* Largest expert count and top-k the layout kernels accept. */
 #define EP_MAX_EXPERTS 1024
@@ -561,6 +576,181 @@ int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const 
                     const int32_t *offsets, int32_t num_experts, int64_t capacity_rows,
                     int32_t out_features, int32_t in_features, int32_t x_dtype,
                     const void *previous, void *dw, int32_t dw_dtype, void *stream);
+
+/*
+ * The router's operators
+ * ----------------------
+ * From a router's logits to the ids and weights that ep_layout, ep_dispatch,
+ * ep_combine and ep_moe_layer take, with the losses that keep the experts
+ * evenly used, and back. Shapes are run-time values (no capability gate); a
+ * workgroup cap of the stream applies and changes no result. Results are a
+ * pure function of the inputs (sums over tokens in a fixed order). No operand
+ * may overlap an output.
+ */
+
+/*
+ * Bytes of device workspace ep_router needs for counts and losses: partial
+ * sums per tile of tokens and sequence. 0 for out-of-range arguments.
+ * Scratch: its contents on entry do not matter; two calls in flight at once
+ * (two streams, two graphs that may replay together) must not share one.
+ */
+size_t ep_router_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_t num_sequences);
+
+/*
+ * Per token t, with its logits l and the scores
+ *   EP_SOFTMAX  s_e = exp(l_e) / sum over j of exp(l_j)
+ *   EP_SIGMOID  s_e = 1 / (1 + exp(-l_e))
+ * topk_idx[t] are the topk experts of the largest l_e, or with select_bias of
+ * the largest s_e + select_bias[e], in descending order; of equal ones the
+ * lowest id first. s + bias is compared as if without rounding errors: sums
+ * that binary32 cannot tell apart are computed again in binary64. An expert whose
+ * logit is -infinity or NaN, or whose bias is -infinity or NaN, is not chosen; where no
+ * more are left, and for a token whose token_mask is 0, the id is -1. Then, for
+ * every id in [0, num_experts) of a token
+ *   topk_weights[t, k] = scale * s_i                          (normalize = 0)
+ *                      = scale * s_i / sum over the token's ids of s_j  (else)
+ * and 0 for other ids. With given != 0, topk_idx is an input instead (ids
+ * outside [0, num_experts) mask their entry, an id may occur twice).
+ *
+ * Unless counts is NULL, over the tokens t of each sequence s, those in
+ * [seq_offsets[s], seq_offsets[s + 1]), that have an id in [0, num_experts)
+ * (n_s tokens; others, masked ones among them, take no part):
+ *   counts[s, e]   = number of their entries with id e
+ *   seq_tokens     = n_s for each s, then the number of sequences with n_s > 0
+ *                    (S'), then the sum of all n_s (n)
+ *   balance_loss   = 1/S' sum over s, e of f_se P_se, f_se = counts[s, e] *
+ *                    num_experts / (topk * n_s), P_se = mean over t of p_te,
+ *                    p_te = s_e / sum over j of s_j: 1 for even use
+ *   z_loss         = mean over the n tokens of (log sum over e of exp(l_e))^2
+ * Losses of no tokens are 0. With one sequence, counts are ep_layout's.
+ * Scores in binary32 (exponentials below 2^-126 may count as 0); sums over tokens in binary32 over at most 256 tokens, and
+ * in binary64 beyond. A token whose logits are all -infinity (or none of whose
+ * chosen ones is above) has p = 0, weights 0 and log sum 0.
+ *
+ *   logits         [num_tokens, num_experts] of dtype (EP_BF16, EP_FP32)
+ *   select_bias    fp32 [num_experts] or NULL; not with given
+ *   token_mask     uint8 [num_tokens] or NULL for no masked token; not with
+ *                  given (mask the ids)
+ *   seq_offsets    int32 [num_sequences + 1], ascending, or NULL for one sequence
+ *                  of all tokens; tokens outside [seq_offsets[0],
+ *                  seq_offsets[num_sequences]) belong to none
+ *   topk           1 .. EP_MAX_TOPK, at most num_experts unless given
+ *   topk_idx       int32 [num_tokens, topk], written unless given
+ *   topk_weights   fp32 [num_tokens, topk] or NULL
+ *   counts         int32 [num_sequences, num_experts] or NULL, with
+ *   seq_tokens     int32 [num_sequences + 2]: both or neither
+ *   balance_loss   fp32 [1] or NULL; with counts
+ *   z_loss         fp32 [1] or NULL; with counts, and EP_SOFTMAX only
+ *   workspace      >= ep_router_workspace_bytes, 16-byte aligned; only with counts
+ * Errors: EP_EINVAL.
+ */
+int ep_router(const void *logits, const float *select_bias, const uint8_t *token_mask,
+              const int32_t *seq_offsets, int32_t num_tokens, int32_t num_experts, int32_t topk,
+              int32_t num_sequences, int32_t dtype, int32_t scoring, int32_t normalize, float scale,
+              int32_t given, int32_t *topk_idx, float *topk_weights, int32_t *counts,
+              int32_t *seq_tokens, float *balance_loss, float *z_loss, void *workspace,
+              size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of ep_router: the logits' gradient, with the ids and counts
+ * held constant, from those of topk_weights, balance_loss and z_loss (each
+ * may be NULL: 0). topk_idx, counts and seq_tokens as the forward pass took
+ * or wrote them (counts and seq_tokens may be NULL without a loss gradient);
+ * dtype, scoring, normalize and scale as given to it. Per token, with dw =
+ * scale * d_topk_weights, s and p as above and q_k = s_k / sum over the
+ * token's ids of s_j, summed over the entries of an id:
+ *   EP_SOFTMAX, normalize   q_k (dw_k - sum over j of q_j dw_j)
+ *   EP_SOFTMAX              p_e (dp_e - sum over j of p_j dp_j), dp_i = dw_i
+ *   EP_SIGMOID, normalize   q_k (1 - s_k) (dw_k - sum over j of q_j dw_j)
+ *   EP_SIGMOID              s_k (1 - s_k) dw_k
+ * and for a token of sequence s that takes part, with g_e = d_balance_loss *
+ * num_experts * counts[s, e] / (topk n_s^2 S'):
+ *   p_e (g_e - sum over j of p_j g_j) (EP_SIGMOID: times 1 - s_e)
+ *   2 d_z_loss / n * log sum exp * p_e
+ * in binary32, rounded once. The logits of a token without ids get 0.
+ *
+ *   d_topk_weights fp32 [num_tokens, topk] or NULL
+ *   d_balance_loss fp32 [1] or NULL
+ *   d_z_loss       fp32 [1] or NULL; EP_SOFTMAX only
+ *   d_logits       [num_tokens, num_experts] of dtype, every element written
+ * Errors: EP_EINVAL.
+ */
+int ep_router_backward(const void *logits, const int32_t *topk_idx, const int32_t *seq_offsets,
+                       const int32_t *counts, const int32_t *seq_tokens,
+                       const float *d_topk_weights, const float *d_balance_loss,
+                       const float *d_z_loss, int32_t num_tokens, int32_t num_experts,
+                       int32_t topk, int32_t num_sequences, int32_t dtype, int32_t scoring,
+                       int32_t normalize, float scale, void *d_logits, void *stream);
+
+/*
+ * The experts' products in 8-bit integers
+ * ---------------------------------------
+ * Rows and weights as 8-bit integers with one fp32 scale per row of the
+ * expand buffer (per token) and per row of a weight matrix (per output
+ * channel). Rules of the experts' operators above. A layer is ep_dispatch
+ * (of rows already quantised, or before it), ep_quantize_rows,
+ * ep_quantized_matmul, ep_swiglu_quantize, ep_quantized_matmul, ep_combine.
+ * Quantised rows move through ep_dispatch as EP_FP8_E4M3 bytes: with
+ * scale_cols = hidden / 128 equal copies of a row's scale they are its scale rows.
+ */
+
+/*
+ * Rows to 8-bit integers, one scale per row, for the experts' rows:
+ *   a = max(2^-100, largest magnitude of the row)
+ *   scales[r, :] = a / 127                (scale_cols equal copies)
+ *   codes[r, i]  = x[r, i] * (127 / a), rounded to the nearest integer, halves to even
+ * where 127 / a is rounded to binary32 and its product with x is not rounded
+ * before the integer: the codes, from -127 to 127, are exactly determined. A
+ * row that holds an infinity or NaN gets the scale NaN and codes 0, so that
+ * its products are NaN.
+ *
+ *   x           [capacity_rows, width] of dtype (EP_BF16, EP_FP32)
+ *   codes       int8 [capacity_rows, width]
+ *   scales      fp32 [capacity_rows, scale_cols]
+ * width is a multiple of 16; scale_cols in 1 .. 2^20. One dense matrix (token
+ * rows, or a weight matrix): num_experts 1 and NULL counts, offsets. Errors: EP_EINVAL.
+ */
+int ep_quantize_rows(const void *x, const int32_t *counts, const int32_t *offsets,
+                     int32_t num_experts, int64_t capacity_rows, int32_t width, int32_t dtype,
+                     void *codes, float *scales, int32_t scale_cols, void *stream);
+
+/*
+ * The experts' gated activation, quantised: ep_quantize_rows of
+ *   h = gate / (1 + exp(-gate)) * up
+ * in binary32 (gates below -87 as in ep_swiglu), h not rounded to the rows'
+ * type in between.
+ *
+ *   gate_up     [capacity_rows, 2 * intermediate] of dtype (EP_BF16, EP_FP32)
+ *   codes       int8 [capacity_rows, intermediate]
+ *   scales      fp32 [capacity_rows, scale_cols]
+ * intermediate is a multiple of 16. Errors: EP_EINVAL.
+ */
+int ep_swiglu_quantize(const void *gate_up, const int32_t *counts, const int32_t *offsets,
+                       int32_t num_experts, int64_t capacity_rows, int32_t intermediate,
+                       int32_t dtype, void *codes, float *scales, int32_t scale_cols,
+                       void *stream);
+
+/*
+ * Per-expert products of 8-bit integers, for any number of rows:
+ *   y[r, n] = x_scales[r, 0] * w_scales[e, n] * sum over k of x[r, k] w[e, n, k]
+ * for the rows r of each expert e. The sum is exact in 32 bits (all 256 codes
+ * are allowed); it is rounded to binary32, scaled by the row's and then the
+ * channel's scale, and rounded once to y's type.
+ *
+ *   x             int8 [capacity_rows, in_features], an expand buffer
+ *   x_scales      fp32 [capacity_rows, x_scale_cols], of which the first column is read
+ *   w             int8 [num_experts, out_features, in_features]; one expert's
+ *                 matrix is below 2^31 bytes
+ *   w_scales      fp32 [num_experts, out_features]
+ *   y             [capacity_rows, out_features] of y_dtype (EP_BF16, EP_FP32)
+ * in_features is a multiple of 16 up to EP_MAX_QUANTIZED_WIDTH, out_features
+ * a multiple of 8 up to 2^24. One dense matrix: num_experts 1 and NULL counts, offsets. Errors:
+ * EP_EINVAL.
+ */
+int ep_quantized_matmul(const void *x, const float *x_scales, int32_t x_scale_cols, const void *w,
+                        const float *w_scales, const int32_t *counts, const int32_t *offsets,
+                        int32_t num_experts, int64_t capacity_rows, int32_t in_features,
+                        int32_t out_features, void *y, int32_t y_dtype, void *stream);
 
 /*
  * CU-limited mode ("MORI JIT v2" section 5.1: geometry buckets prefer the
