@@ -1,60 +1,256 @@
 // The experts' products in 8-bit integers on the expand layout for gfx950:
 // y[r, n] = x_scales[r] * w_scales[e, n] * sum over k of x[r, k] w[e, n, k].
+#include <type_traits>
+
 #include "ep_device.hpp"
 #include "ep_launch.hpp"
 
 namespace ep {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef const __attribute__((address_space(3))) void lds_void;
 
-constexpr int kThreads = 256;
-constexpr uint32_t kOutside = 0x80000000u;
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+constexpr uint32_t kOutside = 0x80000000u;  // an offset outside every descriptor (below 2^30 bytes here)
+constexpr uint32_t kBehind = 0x40000000u;   // added to an offset, outside too; to kOutside as well
+constexpr int kXcds = 8;
+constexpr int kStep = 64;                   // values of the long axis per step
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
   constexpr int kRawBufferFlags = 0x00020000;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes,
                                            kRawBufferFlags);
 }
-__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t off) {
-  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+__device__ __forceinline__ const char *uniform(const char *p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return (const char *)((uint64_t)hi << 32 | lo);
+}
+// 16 bytes per lane from memory to 1 KB of LDS at `to` (the same in every lane), lane after lane;
+// an offset outside the descriptor writes zeros. In assembly, because the compiler waits for every
+// load on its way before it reads LDS, whatever place the load writes: the waits are the kernel's own.
+// Nothing else here uses m0, which holds the place.
+__device__ __forceinline__ uint32_t lds_at(const void *p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uintptr_t)(lds_void *)p);
+}
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
 
-// A wave takes 16 rows by 16 channels, four waves 64 channels.
-__global__ __launch_bounds__(kThreads) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a, int tiles_n,
-                                                                      int64_t units) {
-  const int lane = lane_id(), r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int e = (int)(u / tiles_n), n0 = (int)(u % tiles_n) * 64 + wave * 16;
-    int begin = 0, count = (int)a.capacity;
-    if (a.counts != nullptr) {
-      begin = __builtin_amdgcn_readfirstlane(a.offsets[e]);
-      count = clip_span(begin, __builtin_amdgcn_readfirstlane(a.counts[e]), a.capacity);
+// A wave's tile: 128 rows of x by 128 channels, as 4 x 4 products of 32 x 32.
+constexpr int kSide = 128, kBlocks = kSide / 32;
+
+// WM x (4 / WM) waves.
+template <int WM>
+struct Shape {
+  static constexpr int kWN = kWaves / WM;
+  static constexpr int kRows = WM * kSide, kCols = kWN * kSide;
+  static constexpr int kStageBytes = (kRows + kCols) * kStep;
+  static constexpr int kStages = 4;
+};
+
+// Tiles of the experts before e, for every e: a workgroup's own prefix sums in LDS.
+template <class F>
+__device__ __forceinline__ void prefix_tiles(int *before, int *wave_sums, int E, F tiles) {
+  const int per = (E + kThreads - 1) / kThreads, first = threadIdx.x * per;
+  int own = 0;
+  for (int i = 0; i < per; ++i)
+    if (first + i < E) own += tiles(first + i);
+  const int upto = wave_inclusive_scan(own);
+  const int wave = threadIdx.x / kWave;
+  if ((threadIdx.x & (kWave - 1)) == kWave - 1) wave_sums[wave] = upto;
+  __syncthreads();
+  int sum = upto - own;
+  for (int w = 0; w < wave; ++w) sum += wave_sums[w];
+  for (int i = 0; i < per; ++i)
+    if (first + i < E) {
+      before[first + i] = sum;
+      sum += tiles(first + i);
     }
-    const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w + (int64_t)e * a.N * a.K, (int64_t)a.N * a.K);
-    const uint32_t wrow = n0 + r < a.N ? (uint32_t)(n0 + r) * (uint32_t)a.K : kOutside;
-    for (int m0 = 0; m0 < count; m0 += 16) {
-      const int rows = count - m0 < 16 ? count - m0 : 16;
-      const int64_t first = (int64_t)begin + m0;
-      const __amdgpu_buffer_rsrc_t x = buffer_of((const char *)a.x + first * a.K, (int64_t)rows * a.K);
-      i32x4 acc = {0, 0, 0, 0};
-      for (int k = 0; k < a.K; k += 64) {
-        const bool in = k + g * 16 < a.K;
-        const i32x4 av = load16(w, in ? wrow + (uint32_t)(k + g * 16) : kOutside);
-        const i32x4 bv = load16(x, in && r < rows ? (uint32_t)r * (uint32_t)a.K + (uint32_t)(k + g * 16) : kOutside);
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, acc, 0, 0, 0);
-      }
-      if (r >= rows) continue;
-      const float sx = a.x_scales[(first + r) * a.x_scale_cols];
+  if (threadIdx.x == kThreads - 1) before[E] = sum;
+  __syncthreads();
+}
+
+template <int WM, bool FP32>
+__global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a) {
+  using S = Shape<WM>;
+  constexpr int kXBlocks = S::kRows / 16 / kWaves, kWBlocks = S::kCols / 16 / kWaves;  // per wave, of 16 rows
+  constexpr int kLoads = kXBlocks + kWBlocks;
+  constexpr int kElt = FP32 ? 4 : 2, kStrideOut = kSide * kElt + 16;
+  static_assert(kWaves * 32 * kStrideOut <= S::kStages * S::kStageBytes, "results pass through the stages");
+  __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
+  __shared__ int before[EP_MAX_EXPERTS + 1];
+  __shared__ int wave_sums[kWaves];
+  const int lane = lane_id(), r32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave % WM * kSide, wn = wave / WM * kSide;
+  const int N = a.N, K = a.K;
+  const uint32_t stages = lds_at(lds);
+  const int tiles_n = (N + S::kCols - 1) / S::kCols, steps = (K + kStep - 1) / kStep;
+  const auto span = [&](int e, int &begin) {
+    if (a.counts == nullptr) {
+      begin = 0;
+      return (int)a.capacity;
+    }
+    begin = a.offsets[e];
+    const int n = clip_span(begin, a.counts[e], a.capacity);
+    return n > 0 ? n : 0;
+  };
+  prefix_tiles(before, wave_sums, a.E, [&](int e) {
+    int b;
+    return (span(e, b) + S::kRows - 1) / S::kRows * tiles_n;
+  });
+  const int units = __builtin_amdgcn_readfirstlane(before[a.E]);
+  // Workgroup b runs on XCD b % 8: each XCD takes a run of consecutive units.
+  const int xcd = blockIdx.x % kXcds, group = blockIdx.x / kXcds, groups = (gridDim.x + kXcds - 1 - xcd) / kXcds;
+  const int64_t active = gridDim.x < kXcds ? gridDim.x : kXcds;
+  const int u1 = (int)(units * (xcd + 1) / active);
+  for (int u = (int)(units * xcd / active) + group; u < u1; u += groups) {
+    int lo = 0, hi = a.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    int begin;
+    const int count = __builtin_amdgcn_readfirstlane(span(e, begin));
+    const int t = u - __builtin_amdgcn_readfirstlane(before[e]), tiles_m = (count + S::kRows - 1) / S::kRows;
+    if (t < 0 || t >= tiles_m * tiles_n) continue;  // spans that overlap so often that their tiles pass 2^31
+    constexpr int kTall = 4;  // row tiles side by side before the next column tile
+    const int tall = t / (kTall * tiles_n), left = tiles_m - tall * kTall, width = left < kTall ? left : kTall;
+    const int in = t - tall * kTall * tiles_n;
+    const int m0 = (tall * kTall + in % width) * S::kRows, n0 = in / width * S::kCols;
+    const int rows = count - m0 < S::kRows ? count - m0 : S::kRows, cols = N - n0 < S::kCols ? N - n0 : S::kCols;
+    const int64_t first = (int64_t)begin + m0;
+    const __amdgpu_buffer_rsrc_t bx = buffer_of(uniform((const char *)a.x + first * K), (int64_t)rows * K);
+    const __amdgpu_buffer_rsrc_t bw =
+        buffer_of(uniform((const char *)a.w + ((int64_t)e * N + n0) * K), (int64_t)cols * K);
+    // A load brings 64 bytes of 16 rows; lane l takes row l / 4 and the 16 bytes (l % 4) ^ (l / 16) of
+    // it, so that the 16 bytes of one place in 16 rows, which are read together, lie in different banks.
+    const int piece = ((lane & 3) ^ (lane >> 4)) * 16;
+    uint32_t off[kLoads];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = n0 + g * 4 + i;
-        if (n >= a.N) continue;
-        const float v = (float)acc[i] * sx * a.w_scales[(int64_t)e * a.N + n];
-        if (a.fp32) ((float *)a.y)[(first + r) * a.N + n] = v;
-        else ((__bf16 *)a.y)[(first + r) * a.N + n] = (__bf16)v;
+    for (int i = 0; i < kLoads; ++i) {
+      const bool of_x = i < kXBlocks;
+      const int row = (of_x ? wave * kXBlocks + i : wave * kWBlocks + i - kXBlocks) * 16 + (lane >> 2);
+      off[i] = row < (of_x ? rows : cols) ? (uint32_t)row * (uint32_t)K : kOutside;
+    }
+    const auto load = [&](int step, int slot) {
+      const uint32_t at = step * kStep + piece;
+      const uint32_t k = at < (uint32_t)K ? at : kBehind;
+      const uint32_t to = stages + slot * S::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const bool of_x = i < kXBlocks;
+        const int block = of_x ? wave * kXBlocks + i : S::kRows / 16 + wave * kWBlocks + i - kXBlocks;
+        load_to_lds(of_x ? bx : bw, off[i] + k, to + block * 1024);
       }
+    };
+    i32x16 acc[kBlocks][kBlocks];  // [channels][rows]
+#pragma unroll
+    for (int p = 0; p < kBlocks; ++p)
+#pragma unroll
+      for (int q = 0; q < kBlocks; ++q) acc[p][q] = i32x16{};
+    struct Operands {
+      i32x4 w[kBlocks], x[kBlocks];
+    };
+    const int turn = r32 >> 2 & 3;
+    const int at_x = (wm + r32) * kStep, at_w = (S::kRows + wn + r32) * kStep;
+    const auto fetch = [&](int slot, int part, Operands &o) {
+      const char *const from = lds + slot * S::kStageBytes + (((2 * part + half) ^ turn) * 16);
+#pragma unroll
+      for (int p = 0; p < kBlocks; ++p) o.w[p] = *(const i32x4 *)(from + at_w + p * 32 * kStep);
+#pragma unroll
+      for (int q = 0; q < kBlocks; ++q) o.x[q] = *(const i32x4 *)(from + at_x + q * 32 * kStep);
+    };
+    const auto multiply = [&](const Operands &o) {
+#pragma unroll
+      for (int p = 0; p < kBlocks; ++p)
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q)
+          acc[p][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[p], o.x[q], acc[p][q], 0, 0, 0);
+    };
+    // Before step t's operands are read its loads have to be there (those of the two steps behind it
+    // may be on their way), and every wave has left step t - 1, whose place the next loads take.
+    const auto arrive = [&] {
+      static_assert(kLoads == 8, "two steps behind");
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto spread = [&] {  // an LDS read, then two products
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      }
+    };
+    __syncthreads();  // the last unit's results have left the stages
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) load(s, s);
+    Operands even, odd;
+    arrive();
+    fetch(0, 0, even);
+    load(S::kStages - 1, S::kStages - 1);
+    fetch(0, 1, odd);
+    multiply(even);
+    for (int s = 1; s < steps; ++s) {
+      arrive();
+      fetch(s % S::kStages, 0, even);
+      load(s + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
+      multiply(odd);
+      spread();
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(s % S::kStages, 1, odd);
+      multiply(even);
+      spread();
+    }
+    multiply(odd);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // Results leave through LDS, 32 rows of a wave's 128 channels at a time, as whole lines.
+    const __amdgpu_buffer_rsrc_t bs = buffer_of(uniform((const char *)(a.w_scales + (int64_t)e * N + n0)), (int64_t)cols * 4);
+    char *const mine = lds + wave * 32 * kStrideOut;
+#pragma unroll
+    for (int q = 0; q < kBlocks; ++q) {
+      const int row = wm + q * 32 + r32;
+      const float sx = row < rows ? a.x_scales[(first + row) * a.x_scale_cols] : 0.f;
+#pragma unroll
+      for (int p = 0; p < kBlocks; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = p * 32 + i * 8 + half * 4;
+          const f32x4 sw = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(bs, (wn + n) * 4, 0, 0));
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = (float)acc[p][q][i * 4 + j] * sx * sw[j];
+          char *const to = mine + r32 * kStrideOut + n * kElt;
+          if constexpr (FP32) *(f32x4 *)to = v;
+          else *(u32x2 *)to = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      constexpr int kLanes = kSide * kElt / 16, kPasses = 32 * kLanes / kWave;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int r = i * (kWave / kLanes) + lane / kLanes, c = lane % kLanes * (16 / kElt);
+        const u32x4 v = *(const u32x4 *)(mine + r * kStrideOut + c * kElt);
+        const int row_out = wm + q * 32 + r;
+        if (row_out < rows && wn + c < cols)
+          *(u32x4 *)((char *)a.y + ((first + row_out) * N + n0 + wn + c) * kElt) = v;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
   }
 }
@@ -64,9 +260,9 @@ __global__ __launch_bounds__(kThreads) void ep_quantized_matmul_tiles(const Quan
 int launch_quantized_matmul(const QuantizedMatmulArgs &a) {
   if (a.capacity == 0) return 0;
   const int cap = stream_workgroup_limit(a.stream);
-  const int tiles_n = (a.N + 63) / 64;
-  const int64_t units = (int64_t)a.E * tiles_n, most = cap > 0 ? cap : 1 << 22;
-  ep_quantized_matmul_tiles<<<(unsigned)(units < most ? units : most), kThreads, 0, a.stream>>>(a, tiles_n, units);
+  const unsigned grid = cap > 0 && cap < 256 ? cap : 256;
+  if (a.fp32) ep_quantized_matmul_tiles<2, true><<<grid, kThreads, 0, a.stream>>>(a);
+  else ep_quantized_matmul_tiles<2, false><<<grid, kThreads, 0, a.stream>>>(a);
   return launch_status();
 }
 
