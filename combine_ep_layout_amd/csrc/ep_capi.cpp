@@ -1093,8 +1093,8 @@ int ep_quantized_matmul(const void *x, const float *x_scales, int32_t x_scale_co
     if (in_features < 16 || in_features % 16 != 0 || in_features > EP_MAX_QUANTIZED_WIDTH)
       return fail(EP_EINVAL, "%s: in_features must be a positive multiple of 16 up to %d (got %d)",
                   what, EP_MAX_QUANTIZED_WIDTH, in_features);
-    if (out_features < 8 || out_features % 8 != 0 || out_features > (1 << 24))
-      return fail(EP_EINVAL, "%s: out_features must be a positive multiple of 8 up to 2^24 (got %d)",
+    if (out_features < 8 || out_features % 8 != 0 || out_features > (1 << 23))
+      return fail(EP_EINVAL, "%s: out_features must be a positive multiple of 8 up to 2^23 (got %d)",
                   what, out_features);
     if ((int64_t)in_features * out_features > INT32_MAX)
       return fail(EP_EINVAL, "%s: one expert's w has %lld bytes, 2^31 or more", what,

@@ -20,7 +20,7 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr uint32_t kOutside = 0x80000000u;  // an offset outside every descriptor (below 2^30 bytes here)
 constexpr uint32_t kBehind = 0x40000000u;   // added to an offset, outside too; to kOutside as well
 constexpr int kXcds = 8;
-constexpr int kStep = 64;                   // values of the long axis per step
+constexpr int kStep = 128;                  // values of the long axis per step: a cache line of a row
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, int64_t bytes) {
   constexpr int kRawBufferFlags = 0x00020000;
@@ -58,7 +58,7 @@ struct Shape {
   static constexpr int kWN = kWaves / WM;
   static constexpr int kRows = WM * kSide, kCols = kWN * kSide;
   static constexpr int kStageBytes = (kRows + kCols) * kStep;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 2;
 };
 
 // Tiles of the experts before e, for every e: a workgroup's own prefix sums in LDS.
@@ -86,7 +86,7 @@ __device__ __forceinline__ void prefix_tiles(int *before, int *wave_sums, int E,
 template <int WM, bool FP32>
 __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a) {
   using S = Shape<WM>;
-  constexpr int kXBlocks = S::kRows / 16 / kWaves, kWBlocks = S::kCols / 16 / kWaves;  // per wave, of 16 rows
+  constexpr int kXBlocks = S::kRows / 8 / kWaves, kWBlocks = S::kCols / 8 / kWaves;  // per wave, of 8 rows
   constexpr int kLoads = kXBlocks + kWBlocks;
   constexpr int kElt = FP32 ? 4 : 2, kStrideOut = kSide * kElt + 16;
   static_assert(kWaves * 32 * kStrideOut <= S::kStages * S::kStageBytes, "results pass through the stages");
@@ -138,25 +138,30 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
     const __amdgpu_buffer_rsrc_t bx = buffer_of(uniform((const char *)a.x + first * K), (int64_t)rows * K);
     const __amdgpu_buffer_rsrc_t bw =
         buffer_of(uniform((const char *)a.w + ((int64_t)e * N + n0) * K), (int64_t)cols * K);
-    // A load brings 64 bytes of 16 rows; lane l takes row l / 4 and the 16 bytes (l % 4) ^ (l / 16) of
+    // A load brings a line of 8 rows. Lane l takes row l / 8 and the 16 bytes (l % 8) ^ (row / 2 % 8) of
     // it, so that the 16 bytes of one place in 16 rows, which are read together, lie in different banks.
-    const int piece = ((lane & 3) ^ (lane >> 4)) * 16;
+    const int piece = ((lane & 7) ^ (lane >> 4)) * 16;  // of even blocks; 64 bytes off in odd ones
     uint32_t off[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const bool of_x = i < kXBlocks;
-      const int row = (of_x ? wave * kXBlocks + i : wave * kWBlocks + i - kXBlocks) * 16 + (lane >> 2);
+      const int row = (of_x ? wave * kXBlocks + i : wave * kWBlocks + i - kXBlocks) * 8 + (lane >> 3);
       off[i] = row < (of_x ? rows : cols) ? (uint32_t)row * (uint32_t)K : kOutside;
     }
-    const auto load = [&](int step, int slot) {
-      const uint32_t at = step * kStep + piece;
-      const uint32_t k = at < (uint32_t)K ? at : kBehind;
-      const uint32_t to = stages + slot * S::kStageBytes;
+    const auto load = [&](int step, int from, int to) {  // the loads [from, to) of a step
+      uint32_t k[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = step * kStep + (piece ^ i * 64);
+        k[i] = at < (uint32_t)K ? at : kBehind;
+      }
+      const uint32_t place = stages + (step & 1) * S::kStageBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
+        if (i < from || i >= to) continue;
         const bool of_x = i < kXBlocks;
-        const int block = of_x ? wave * kXBlocks + i : S::kRows / 16 + wave * kWBlocks + i - kXBlocks;
-        load_to_lds(of_x ? bx : bw, off[i] + k, to + block * 1024);
+        const int block = of_x ? wave * kXBlocks + i : S::kRows / 8 + wave * kWBlocks + i - kXBlocks;
+        load_to_lds(of_x ? bx : bw, off[i] + k[i & 1], place + block * 1024);
       }
     };
     i32x16 acc[kBlocks][kBlocks];  // [channels][rows]
@@ -167,10 +172,10 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
     struct Operands {
       i32x4 w[kBlocks], x[kBlocks];
     };
-    const int turn = r32 >> 2 & 3;
+    const int turn = r32 >> 1 & 7;
     const int at_x = (wm + r32) * kStep, at_w = (S::kRows + wn + r32) * kStep;
-    const auto fetch = [&](int slot, int part, Operands &o) {
-      const char *const from = lds + slot * S::kStageBytes + (((2 * part + half) ^ turn) * 16);
+    const auto fetch = [&](int step, int part, Operands &o) {
+      const char *const from = lds + (step & 1) * S::kStageBytes + (((2 * part + half) ^ turn) * 16);
 #pragma unroll
       for (int p = 0; p < kBlocks; ++p) o.w[p] = *(const i32x4 *)(from + at_w + p * 32 * kStep);
 #pragma unroll
@@ -182,44 +187,38 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
 #pragma unroll
         for (int q = 0; q < kBlocks; ++q)
           acc[p][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[p], o.x[q], acc[p][q], 0, 0, 0);
-    };
-    // Before step t's operands are read its loads have to be there (those of the two steps behind it
-    // may be on their way), and every wave has left step t - 1, whose place the next loads take.
-    const auto arrive = [&] {
-      static_assert(kLoads == 8, "two steps behind");
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    const auto spread = [&] {  // an LDS read, then two products
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {  // an LDS read, then two products
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Before a step's operands are read its loads have to be there, and every wave has read the step
+    // before it, whose place the next loads take.
+    const auto arrive = [&] {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
     };
     __syncthreads();  // the last unit's results have left the stages
-#pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) load(s, s);
+    load(0, 0, kLoads);
     Operands even, odd;
     arrive();
     fetch(0, 0, even);
-    load(S::kStages - 1, S::kStages - 1);
-    fetch(0, 1, odd);
-    multiply(even);
-    for (int s = 1; s < steps; ++s) {
-      arrive();
-      fetch(s % S::kStages, 0, even);
-      load(s + S::kStages - 1, (s + S::kStages - 1) % S::kStages);
-      multiply(odd);
-      spread();
-      __builtin_amdgcn_sched_barrier(0);
-      fetch(s % S::kStages, 1, odd);
+    for (int s = 0; s < steps; ++s) {
+      load(s + 1, 0, kLoads / 2);
+      fetch(s, 1, odd);
       multiply(even);
-      spread();
+      load(s + 1, kLoads / 2, kLoads);
+      fetch(s, 2, even);
+      multiply(odd);
+      fetch(s, 3, odd);
+      multiply(even);
+      arrive();
+      fetch(s + 1, 0, even);  // behind the last step: zeros that are not used
+      multiply(odd);
     }
-    multiply(odd);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // Results leave through LDS, 32 rows of a wave's 128 channels at a time, as whole lines.
     const __amdgpu_buffer_rsrc_t bs = buffer_of(uniform((const char *)(a.w_scales + (int64_t)e * N + n0)), (int64_t)cols * 4);
     char *const mine = lds + wave * 32 * kStrideOut;
@@ -241,14 +240,19 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
           else *(u32x2 *)to = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
         }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int here = rows - wm - q * 32 < 32 ? rows - wm - q * 32 : 32;
+      // a wave whose rows or channels all lie behind the end stores nothing: a descriptor of no bytes
+      const __amdgpu_buffer_rsrc_t by =
+          buffer_of(uniform((const char *)a.y + ((first + wm + q * 32) * N + n0 + wn) * kElt),
+                    here > 0 && wn < cols ? ((int64_t)(here - 1) * N + cols - wn) * kElt : 0);
       constexpr int kLanes = kSide * kElt / 16, kPasses = 32 * kLanes / kWave;
+      const int c = lane % kLanes * (16 / kElt);
+      uint32_t off_y = wn + c < cols ? (uint32_t)(lane / kLanes * N + c) * kElt : kOutside;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int r = i * (kWave / kLanes) + lane / kLanes, c = lane % kLanes * (16 / kElt);
-        const u32x4 v = *(const u32x4 *)(mine + r * kStrideOut + c * kElt);
-        const int row_out = wm + q * 32 + r;
-        if (row_out < rows && wn + c < cols)
-          *(u32x4 *)((char *)a.y + ((first + row_out) * N + n0 + wn + c) * kElt) = v;
+        const u32x4 v = *(const u32x4 *)(mine + (i * (kWave / kLanes) + lane / kLanes) * kStrideOut + c * kElt);
+        __builtin_amdgcn_raw_buffer_store_b128(v, by, (int)off_y, 0, 0);
+        off_y += (uint32_t)(kWave / kLanes * N) * kElt;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }

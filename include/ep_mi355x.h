@@ -744,7 +744,7 @@ int ep_swiglu_quantize(const void *gate_up, const int32_t *counts, const int32_t
  *   w_scales      fp32 [num_experts, out_features]
  *   y             [capacity_rows, out_features] of y_dtype (EP_BF16, EP_FP32)
  * in_features is a multiple of 16 up to EP_MAX_QUANTIZED_WIDTH, out_features
- * a multiple of 8 up to 2^24. One dense matrix: num_experts 1 and NULL counts, offsets. Errors:
+ * a multiple of 8 up to 2^23. One dense matrix: num_experts 1 and NULL counts, offsets. Errors:
  * EP_EINVAL.
  */
 int ep_quantized_matmul(const void *x, const float *x_scales, int32_t x_scale_cols, const void *w,

@@ -110,7 +110,7 @@ def matmul(**kw):
 
 
 MATMUL = [dict(E=0), dict(E=1025), dict(cap=-1), dict(cap=1 << 31), dict(c=None), dict(o=None), dict(c=None, o=None), dict(K=0),
-          dict(K=8), dict(K=200), dict(K=131072), dict(N=0), dict(N=12), dict(N=(1 << 24) + 8), dict(K=65536, N=32768), dict(cols=0),
+          dict(K=8), dict(K=200), dict(K=131072), dict(N=0), dict(N=12), dict(N=(1 << 23) + 8), dict(K=65536, N=32768), dict(cols=0),
           dict(cols=1 << 21), dict(yd=B.EP_FP8_E4M3), dict(yd=5), dict(x=None), dict(s=None), dict(w=None), dict(ws=None), dict(y=None),
           dict(x=ODD), dict(w=ODD), dict(y=ODD), dict(s=FAKE + 2), dict(ws=FAKE + 1), dict(c=FAKE + 2)]
 
