@@ -44,22 +44,21 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
                : "memory");
 }
+// 4 bytes per lane to 256 bytes of LDS.
+__device__ __forceinline__ void touch(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const f32x2 f = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
 
-// A wave's tile: 128 rows of x by 128 channels, as 4 x 4 products of 32 x 32.
-constexpr int kSide = 128, kBlocks = kSide / 32;
-
-// WM x (4 / WM) waves.
-template <int WM>
-struct Shape {
-  static constexpr int kWN = kWaves / WM;
-  static constexpr int kRows = WM * kSide, kCols = kWN * kSide;
-  static constexpr int kStageBytes = (kRows + kCols) * kStep;
-  static constexpr int kStages = 2;
-};
+// A workgroup's tile: 256 rows by 256 channels, a quarter for each of four waves: 128 channels (four
+// blocks of 32) and every second block of 32 rows, so that a tile of few rows is shared out evenly.
+constexpr int kSide = 256, kBlock = 32, kBlocks = 4;
+constexpr int kOperandBytes = kSide * kStep, kStageBytes = 2 * kOperandBytes;  // of a step: x, then w
+constexpr int kLineOut = 128, kStrideOut = kLineOut + 16;  // results leave by lines of 32 rows
 
 // Tiles of the experts before e, for every e: a workgroup's own prefix sums in LDS.
 template <class F>
@@ -83,22 +82,26 @@ __device__ __forceinline__ void prefix_tiles(int *before, int *wave_sums, int E,
   __syncthreads();
 }
 
-template <int WM, bool FP32>
+struct Unit {
+  int e, rows, cols, n0;
+  int64_t first;  // row of the buffer
+};
+
+template <bool FP32>
 __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a) {
-  using S = Shape<WM>;
-  constexpr int kXBlocks = S::kRows / 8 / kWaves, kWBlocks = S::kCols / 8 / kWaves;  // per wave, of 8 rows
-  constexpr int kLoads = kXBlocks + kWBlocks;
-  constexpr int kElt = FP32 ? 4 : 2, kStrideOut = kSide * kElt + 16;
-  static_assert(kWaves * 32 * kStrideOut <= S::kStages * S::kStageBytes, "results pass through the stages");
-  __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStageBytes];
+  constexpr int kLoads = kSide / 8 / kWaves;  // of a wave per operand and step: a line of 8 rows each
+  constexpr int kElt = FP32 ? 4 : 2;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+  __shared__ __attribute__((aligned(16))) char lines[kWaves * kBlock * kStrideOut];
+  __shared__ __attribute__((aligned(16))) float scales[3][2][kSide];  // of x's rows and of channels, for three units in turn
+  __shared__ int sink[kThreads];
   __shared__ int before[EP_MAX_EXPERTS + 1];
   __shared__ int wave_sums[kWaves];
   const int lane = lane_id(), r32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave % WM * kSide, wn = wave / WM * kSide;
+  const int wm = (wave & 1) * kBlock, wn = (wave >> 1) * (kSide / 2);
   const int N = a.N, K = a.K;
-  const uint32_t stages = lds_at(lds);
-  const int tiles_n = (N + S::kCols - 1) / S::kCols, steps = (K + kStep - 1) / kStep;
+  const int tiles_n = (N + kSide - 1) / kSide, steps = (K + kStep - 1) / kStep;
   const auto span = [&](int e, int &begin) {
     if (a.counts == nullptr) {
       begin = 0;
@@ -110,153 +113,197 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   };
   prefix_tiles(before, wave_sums, a.E, [&](int e) {
     int b;
-    return (span(e, b) + S::kRows - 1) / S::kRows * tiles_n;
+    return (span(e, b) + kSide - 1) / kSide * tiles_n;
   });
   const int units = __builtin_amdgcn_readfirstlane(before[a.E]);
   // Workgroup b runs on XCD b % 8: each XCD takes a run of consecutive units.
   const int xcd = blockIdx.x % kXcds, group = blockIdx.x / kXcds, groups = (gridDim.x + kXcds - 1 - xcd) / kXcds;
   const int64_t active = gridDim.x < kXcds ? gridDim.x : kXcds;
-  const int u1 = (int)(units * (xcd + 1) / active);
-  for (int u = (int)(units * xcd / active) + group; u < u1; u += groups) {
-    int lo = 0, hi = a.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (before[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
+  const int u1 = (int)(units * (int64_t)(xcd + 1) / active);
+  int u = (int)(units * (int64_t)xcd / active) + group;
+  if (u >= u1) return;
+  // Unit v, for an expert that is not before `from`.
+  const auto locate = [&](int v, int from) {
+    Unit t{from, 0, 0, 0, 0};
+    while (t.e + 1 < a.E && __builtin_amdgcn_readfirstlane(before[t.e + 1]) <= v) ++t.e;
     int begin;
-    const int count = __builtin_amdgcn_readfirstlane(span(e, begin));
-    const int t = u - __builtin_amdgcn_readfirstlane(before[e]), tiles_m = (count + S::kRows - 1) / S::kRows;
-    if (t < 0 || t >= tiles_m * tiles_n) continue;  // spans that overlap so often that their tiles pass 2^31
+    const int count = __builtin_amdgcn_readfirstlane(span(t.e, begin)), tiles_m = (count + kSide - 1) / kSide;
+    const int i = v - __builtin_amdgcn_readfirstlane(before[t.e]);
+    if (i < 0 || i >= tiles_m * tiles_n) return t;  // spans that overlap so often that their tiles pass 2^31
     constexpr int kTall = 4;  // row tiles side by side before the next column tile
-    const int tall = t / (kTall * tiles_n), left = tiles_m - tall * kTall, width = left < kTall ? left : kTall;
-    const int in = t - tall * kTall * tiles_n;
-    const int m0 = (tall * kTall + in % width) * S::kRows, n0 = in / width * S::kCols;
-    const int rows = count - m0 < S::kRows ? count - m0 : S::kRows, cols = N - n0 < S::kCols ? N - n0 : S::kCols;
-    const int64_t first = (int64_t)begin + m0;
-    const __amdgpu_buffer_rsrc_t bx = buffer_of(uniform((const char *)a.x + first * K), (int64_t)rows * K);
-    const __amdgpu_buffer_rsrc_t bw =
-        buffer_of(uniform((const char *)a.w + ((int64_t)e * N + n0) * K), (int64_t)cols * K);
-    // A load brings a line of 8 rows. Lane l takes row l / 8 and the 16 bytes (l % 8) ^ (row / 2 % 8) of
-    // it, so that the 16 bytes of one place in 16 rows, which are read together, lie in different banks.
-    const int piece = ((lane & 7) ^ (lane >> 4)) * 16;  // of even blocks; 64 bytes off in odd ones
-    uint32_t off[kLoads];
+    const int tall = i / (kTall * tiles_n), left = tiles_m - tall * kTall, width = left < kTall ? left : kTall;
+    const int in = i - tall * kTall * tiles_n, m0 = (tall * kTall + in % width) * kSide;
+    t.n0 = in / width * kSide;
+    t.rows = count - m0 < kSide ? count - m0 : kSide, t.cols = N - t.n0 < kSide ? N - t.n0 : kSide;
+    t.first = (int64_t)__builtin_amdgcn_readfirstlane(begin) + m0;
+    return t;
+  };
+  // A unit's operands. A descriptor ends with its last row, so rows behind it read as zeros.
+  const auto rows_of = [&](const Unit &t) {
+    return buffer_of(uniform((const char *)a.x + t.first * K), (int64_t)t.rows * K);
+  };
+  const auto channels_of = [&](const Unit &t) {
+    return buffer_of(uniform((const char *)a.w + ((int64_t)t.e * N + t.n0) * K), (int64_t)t.cols * K);
+  };
+  // A load brings a line of 8 rows. Lane l takes row l / 8 and the 16 bytes (l % 8) ^ (row / 2 % 8) of
+  // it, so that the 16 bytes of one place in 16 rows, which are read together, lie in different banks.
+  const int piece = ((lane & 7) ^ (lane >> 4)) * 16;  // of even loads; 64 bytes off in odd ones
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)((wave * kLoads + i) * 8 + (lane >> 3)) * (uint32_t)K;
+  const uint32_t stages = lds_at(lds), place = stages + wave * kLoads * 1024;
+  const auto load = [&](__amdgpu_buffer_rsrc_t from, int step, uint32_t to) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const bool of_x = i < kXBlocks;
-      const int row = (of_x ? wave * kXBlocks + i : wave * kWBlocks + i - kXBlocks) * 8 + (lane >> 3);
-      off[i] = row < (of_x ? rows : cols) ? (uint32_t)row * (uint32_t)K : kOutside;
+      const uint32_t at = step * kStep + (i & 1 ? piece ^ 64 : piece);
+      load_to_lds(from, off[i] + (at < (uint32_t)K ? at : kBehind), to + i * 1024);
     }
-    const auto load = [&](int step, int from, int to) {  // the loads [from, to) of a step
-      uint32_t k[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t at = step * kStep + (piece ^ i * 64);
-        k[i] = at < (uint32_t)K ? at : kBehind;
-      }
-      const uint32_t place = stages + (step & 1) * S::kStageBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        if (i < from || i >= to) continue;
-        const bool of_x = i < kXBlocks;
-        const int block = of_x ? wave * kXBlocks + i : S::kRows / 8 + wave * kWBlocks + i - kXBlocks;
-        load_to_lds(of_x ? bx : bw, off[i] + k[i & 1], place + block * 1024);
-      }
-    };
-    i32x16 acc[kBlocks][kBlocks];  // [channels][rows]
+  };
+  // Brings the lines of a step of 64 rows into this XCD's L2, two words of LDS that nobody reads.
+  const uint32_t off_ahead = threadIdx.x * (uint32_t)K, nowhere = lds_at(sink + wave * kWave);
+  const auto ahead = [&](__amdgpu_buffer_rsrc_t from, int step) {
+    const uint32_t at = step * kStep;
+    touch(from, off_ahead + (at < (uint32_t)K ? at : kBehind), nowhere);
+  };
+  const auto load_scales = [&](const Unit &t, int turn) {
+    touch(buffer_of(uniform((const char *)(a.x_scales + t.first * a.x_scale_cols)), (int64_t)t.rows * a.x_scale_cols * 4),
+          threadIdx.x * (uint32_t)a.x_scale_cols * 4u, lds_at(scales[turn][0] + wave * kWave));
+    touch(buffer_of(uniform((const char *)(a.w_scales + (int64_t)t.e * N + t.n0)), (int64_t)t.cols * 4), threadIdx.x * 4u,
+          lds_at(scales[turn][1] + wave * kWave));
+  };
+  int e0 = 0;
+  {
+    int hi = a.E;
+    while (hi - e0 > 1) {
+      const int mid = (e0 + hi) / 2;
+      if (__builtin_amdgcn_readfirstlane(before[mid]) <= u) e0 = mid;
+      else hi = mid;
+    }
+  }
+  Unit unit = locate(u, e0), next = unit;
+  __amdgpu_buffer_rsrc_t bx = rows_of(unit), bw = channels_of(unit);
+  int stage = 0, turn = 0;  // of the step, of the unit
+  load_scales(unit, 0);
+  load(bx, 0, place);
+  load(bw, 0, place + kOperandBytes);
+  ahead(bx, 1), ahead(bw, 1);
+  ahead(bx, 2), ahead(bw, 2);
+  asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  const auto tile = [&](auto row_blocks) {
+    constexpr int Q = decltype(row_blocks)::value;  // of every wave
+    i32x16 acc[kBlocks][Q];  // [channels][rows]
 #pragma unroll
     for (int p = 0; p < kBlocks; ++p)
 #pragma unroll
-      for (int q = 0; q < kBlocks; ++q) acc[p][q] = i32x16{};
+      for (int q = 0; q < Q; ++q) acc[p][q] = i32x16{};
     struct Operands {
-      i32x4 w[kBlocks], x[kBlocks];
+      i32x4 w[kBlocks], x[Q];
     };
-    const int turn = r32 >> 1 & 7;
-    const int at_x = (wm + r32) * kStep, at_w = (S::kRows + wn + r32) * kStep;
-    const auto fetch = [&](int step, int part, Operands &o) {
-      const char *const from = lds + (step & 1) * S::kStageBytes + (((2 * part + half) ^ turn) * 16);
+    const int turned = r32 >> 1 & 7;
+    const char *const at = lds + (wm + r32) * kStep;
+    const int to_w = kOperandBytes + (wn - wm) * kStep;
+    const auto fetch = [&](int of, int part, Operands &o) {
+      const char *const from = at + of * kStageBytes + ((2 * part + half) ^ turned) * 16;
 #pragma unroll
-      for (int p = 0; p < kBlocks; ++p) o.w[p] = *(const i32x4 *)(from + at_w + p * 32 * kStep);
+      for (int p = 0; p < kBlocks; ++p) o.w[p] = *(const i32x4 *)(from + to_w + p * kBlock * kStep);
 #pragma unroll
-      for (int q = 0; q < kBlocks; ++q) o.x[q] = *(const i32x4 *)(from + at_x + q * 32 * kStep);
+      for (int q = 0; q < Q; ++q) o.x[q] = *(const i32x4 *)(from + q * 2 * kBlock * kStep);
     };
     const auto multiply = [&](const Operands &o) {
 #pragma unroll
       for (int p = 0; p < kBlocks; ++p)
 #pragma unroll
-        for (int q = 0; q < kBlocks; ++q)
+        for (int q = 0; q < Q; ++q)
           acc[p][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[p], o.x[q], acc[p][q], 0, 0, 0);
+      if constexpr (Q == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // an LDS read, then two products
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        for (int i = 0; i < 8; ++i) {  // an LDS read, then two products
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // Before a step's operands are read its loads have to be there, and every wave has read the step
-    // before it, whose place the next loads take.
-    const auto arrive = [&] {
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    __syncthreads();  // the last unit's results have left the stages
-    load(0, 0, kLoads);
+    const __amdgpu_buffer_rsrc_t next_x = rows_of(next), next_w = channels_of(next);
     Operands even, odd;
-    arrive();
-    fetch(0, 0, even);
+    fetch(stage, 0, even);
     for (int s = 0; s < steps; ++s) {
-      load(s + 1, 0, kLoads / 2);
-      fetch(s, 1, odd);
+      int step = s + 1;
+      if (step == steps) {  // the next unit's first step
+        step = 0, bx = next_x, bw = next_w;
+        load_scales(next, turn < 2 ? turn + 1 : 0);
+      }
+      const uint32_t to = place + (stage ^ 1) * kStageBytes;
+      load(bx, step, to);
+      fetch(stage, 1, odd);
       multiply(even);
-      load(s + 1, kLoads / 2, kLoads);
-      fetch(s, 2, even);
+      load(bw, step, to + kOperandBytes);
+      ahead(s + 3 < steps ? bx : next_x, s + 3 < steps ? s + 3 : s + 3 - steps);
+      ahead(s + 3 < steps ? bw : next_w, s + 3 < steps ? s + 3 : s + 3 - steps);
+      fetch(stage, 2, even);
       multiply(odd);
-      fetch(s, 3, odd);
+      fetch(stage, 3, odd);
       multiply(even);
-      arrive();
-      fetch(s + 1, 0, even);  // behind the last step: zeros that are not used
+      // Before a step's operands are read its loads have to be there (the two that only reach L2
+      // may be on their way: loads return in order), and every wave has read the step before it,
+      // whose place the next loads take.
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      stage ^= 1;
+      fetch(stage, 0, even);  // behind the last step: not used
       multiply(odd);
     }
-    // Results leave through LDS, 32 rows of a wave's 128 channels at a time, as whole lines.
-    const __amdgpu_buffer_rsrc_t bs = buffer_of(uniform((const char *)(a.w_scales + (int64_t)e * N + n0)), (int64_t)cols * 4);
-    char *const mine = lds + wave * 32 * kStrideOut;
+    // Results leave through LDS as whole lines of 32 rows.
+    char *const mine = lines + wave * kBlock * kStrideOut;
+    constexpr int kChannels = kLineOut / kElt, kChunks = kSide / 2 / kChannels;
 #pragma unroll
-    for (int q = 0; q < kBlocks; ++q) {
-      const int row = wm + q * 32 + r32;
-      const float sx = row < rows ? a.x_scales[(first + row) * a.x_scale_cols] : 0.f;
+    for (int q = 0; q < Q; ++q) {
+      const int row0 = wm + q * 2 * kBlock, here = unit.rows - row0 < kBlock ? unit.rows - row0 : kBlock;
+      const float sx = scales[turn][0][row0 + r32];
+      // a wave whose rows or channels all lie behind the end stores nothing: a descriptor of no bytes
+      const __amdgpu_buffer_rsrc_t by =
+          buffer_of(uniform((const char *)a.y + ((unit.first + row0) * N + unit.n0 + wn) * kElt),
+                    here > 0 && wn < unit.cols ? ((int64_t)(here - 1) * N + unit.cols - wn) * kElt : 0);
 #pragma unroll
-      for (int p = 0; p < kBlocks; ++p)
+      for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = p * 32 + i * 8 + half * 4;
-          const f32x4 sw = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(bs, (wn + n) * 4, 0, 0));
+        for (int n = 0; n < kChannels; n += 8) {
+          const int p = (c * kChannels + n) / kBlock, i = n / 8 % 4;
+          const f32x4 sw = *(const f32x4 *)(scales[turn][1] + wn + c * kChannels + n + half * 4);
           f32x4 v;
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = (float)acc[p][q][i * 4 + j] * sx * sw[j];
-          char *const to = mine + r32 * kStrideOut + n * kElt;
+          char *const to = mine + r32 * kStrideOut + (n + half * 4) * kElt;
           if constexpr (FP32) *(f32x4 *)to = v;
           else *(u32x2 *)to = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
         }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const int here = rows - wm - q * 32 < 32 ? rows - wm - q * 32 : 32;
-      // a wave whose rows or channels all lie behind the end stores nothing: a descriptor of no bytes
-      const __amdgpu_buffer_rsrc_t by =
-          buffer_of(uniform((const char *)a.y + ((first + wm + q * 32) * N + n0 + wn) * kElt),
-                    here > 0 && wn < cols ? ((int64_t)(here - 1) * N + cols - wn) * kElt : 0);
-      constexpr int kLanes = kSide * kElt / 16, kPasses = 32 * kLanes / kWave;
-      const int c = lane % kLanes * (16 / kElt);
-      uint32_t off_y = wn + c < cols ? (uint32_t)(lane / kLanes * N + c) * kElt : kOutside;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int col = wn + c * kChannels + lane % 8 * (16 / kElt);
+        uint32_t off_y = col < unit.cols ? (uint32_t)(lane / 8 * N + col - wn) * kElt : kOutside;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const u32x4 v = *(const u32x4 *)(mine + (i * (kWave / kLanes) + lane / kLanes) * kStrideOut + c * kElt);
-        __builtin_amdgcn_raw_buffer_store_b128(v, by, (int)off_y, 0, 0);
-        off_y += (uint32_t)(kWave / kLanes * N) * kElt;
+        for (int i = 0; i < kBlock / 8; ++i) {
+          const u32x4 v = *(const u32x4 *)(mine + (i * 8 + lane / 8) * kStrideOut + lane % 8 * 16);
+          __builtin_amdgcn_raw_buffer_store_b128(v, by, (int)off_y, 0, 0);
+          off_y += (uint32_t)(8 * N) * kElt;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+  };
+  for (;;) {
+    const bool more = u + groups < u1;
+    if (more) next = locate(u + groups, unit.e);
+    else next.rows = next.cols = 0;
+    if (unit.rows > 6 * kBlock) tile(std::integral_constant<int, 4>());
+    else if (unit.rows > 4 * kBlock) tile(std::integral_constant<int, 3>());
+    else if (unit.rows > 2 * kBlock) tile(std::integral_constant<int, 2>());
+    else tile(std::integral_constant<int, 1>());
+    if (!more) break;
+    unit = next, u += groups, turn = turn < 2 ? turn + 1 : 0;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads into this workgroup's LDS
 }
 
 }  // namespace
@@ -265,8 +312,8 @@ int launch_quantized_matmul(const QuantizedMatmulArgs &a) {
   if (a.capacity == 0) return 0;
   const int cap = stream_workgroup_limit(a.stream);
   const unsigned grid = cap > 0 && cap < 256 ? cap : 256;
-  if (a.fp32) ep_quantized_matmul_tiles<2, true><<<grid, kThreads, 0, a.stream>>>(a);
-  else ep_quantized_matmul_tiles<2, false><<<grid, kThreads, 0, a.stream>>>(a);
+  if (a.fp32) ep_quantized_matmul_tiles<true><<<grid, kThreads, 0, a.stream>>>(a);
+  else ep_quantized_matmul_tiles<false><<<grid, kThreads, 0, a.stream>>>(a);
   return launch_status();
 }
 
