@@ -94,7 +94,6 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
   __shared__ __attribute__((aligned(16))) char lines[kWaves * kBlock * kStrideOut];
   __shared__ __attribute__((aligned(16))) float scales[3][2][kSide];  // of x's rows and of channels, for three units in turn
-  __shared__ int sink[kThreads];
   __shared__ int before[EP_MAX_EXPERTS + 1];
   __shared__ int wave_sums[kWaves];
   const int lane = lane_id(), r32 = lane & 31, half = lane >> 5;
@@ -152,19 +151,6 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)((wave * kLoads + i) * 8 + (lane >> 3)) * (uint32_t)K;
   const uint32_t stages = lds_at(lds), place = stages + wave * kLoads * 1024;
-  const auto load = [&](__amdgpu_buffer_rsrc_t from, int step, uint32_t to) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t at = step * kStep + (i & 1 ? piece ^ 64 : piece);
-      load_to_lds(from, off[i] + (at < (uint32_t)K ? at : kBehind), to + i * 1024);
-    }
-  };
-  // Brings the lines of a step of 64 rows into this XCD's L2, two words of LDS that nobody reads.
-  const uint32_t off_ahead = threadIdx.x * (uint32_t)K, nowhere = lds_at(sink + wave * kWave);
-  const auto ahead = [&](__amdgpu_buffer_rsrc_t from, int step) {
-    const uint32_t at = step * kStep;
-    touch(from, off_ahead + (at < (uint32_t)K ? at : kBehind), nowhere);
-  };
   const auto load_scales = [&](const Unit &t, int turn) {
     touch(buffer_of(uniform((const char *)(a.x_scales + t.first * a.x_scale_cols)), (int64_t)t.rows * a.x_scale_cols * 4),
           threadIdx.x * (uint32_t)a.x_scale_cols * 4u, lds_at(scales[turn][0] + wave * kWave));
@@ -180,15 +166,45 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
       else hi = mid;
     }
   }
-  Unit unit = locate(u, e0), next = unit;
-  __amdgpu_buffer_rsrc_t bx = rows_of(unit), bw = channels_of(unit);
+  // What is loaded next: a step of a unit that may be ahead of the one that is multiplied.
+  struct {
+    Unit unit;
+    int u, step, turn;
+    uint32_t place;
+  } ahead{locate(u, e0), u, 0, 0, place};
+  __amdgpu_buffer_rsrc_t ahead_x = rows_of(ahead.unit), ahead_w = channels_of(ahead.unit);
+  const auto advance = [&](int to) {
+    ahead.place = place + to * kStageBytes;
+    if (++ahead.step < steps) return;
+    ahead.step = 0, ahead.u += groups, ahead.turn = ahead.turn < 2 ? ahead.turn + 1 : 0;
+    if (ahead.u < u1) ahead.unit = locate(ahead.u, ahead.unit.e);
+    else ahead.unit.rows = ahead.unit.cols = 0;
+    ahead_x = rows_of(ahead.unit), ahead_w = channels_of(ahead.unit);
+    load_scales(ahead.unit, ahead.turn);
+  };
+  const auto load = [&](int from, int to) {  // of the 2 kLoads loads of a step and wave, x's first
+#pragma unroll
+    for (int d = 0; d < 2 * kLoads; ++d) {
+      if (d < from || d >= to) continue;
+      const int i = d % kLoads;
+      const uint32_t at = ahead.step * kStep + (i & 1 ? piece ^ 64 : piece);
+      load_to_lds(d < kLoads ? ahead_x : ahead_w, off[i] + (at < (uint32_t)K ? at : kBehind),
+                  ahead.place + (d < kLoads ? 0 : kOperandBytes) + i * 1024);
+    }
+  };
+  // A step's loads that are issued by the ends of the last part of the second step before it, and of
+  // the parts of the step before it.
+#ifndef ISSUED
+#define ISSUED 6, 11, 16, 16
+#endif
+  constexpr int kIssued[4] = {ISSUED};
   int stage = 0, turn = 0;  // of the step, of the unit
-  load_scales(unit, 0);
-  load(bx, 0, place);
-  load(bw, 0, place + kOperandBytes);
-  ahead(bx, 1), ahead(bw, 1);
-  ahead(bx, 2), ahead(bw, 2);
-  asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  load_scales(ahead.unit, 0);
+  load(0, 2 * kLoads);
+  advance(1);
+  load(0, kIssued[0]);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kIssued[0]) : "memory");
+  Unit unit{e0, 0, 0, 0, 0};
 
   const auto tile = [&](auto row_blocks) {
     constexpr int Q = decltype(row_blocks)::value;  // of every wave
@@ -203,57 +219,38 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
     const int turned = r32 >> 1 & 7;
     const char *const at = lds + (wm + r32) * kStep;
     const int to_w = kOperandBytes + (wn - wm) * kStep;
-    const auto fetch = [&](int of, int part, Operands &o) {
-      const char *const from = at + of * kStageBytes + ((2 * part + half) ^ turned) * 16;
-#pragma unroll
-      for (int p = 0; p < kBlocks; ++p) o.w[p] = *(const i32x4 *)(from + to_w + p * kBlock * kStep);
-#pragma unroll
-      for (int q = 0; q < Q; ++q) o.x[q] = *(const i32x4 *)(from + q * 2 * kBlock * kStep);
+    const auto fetch = [&](int part, int p, Operands &o) {  // the p-th block of both
+      const char *const from = at + stage * kStageBytes + ((2 * part + half) ^ turned) * 16;
+      o.w[p] = *(const i32x4 *)(from + to_w + p * kBlock * kStep);
+      if (p < Q) o.x[p] = *(const i32x4 *)(from + p * 2 * kBlock * kStep);
     };
-    const auto multiply = [&](const Operands &o) {
+    // Products of one part of a step, and between them the reads of the next part's operands and the
+    // loads [from, to), a few at a time: a wave that waits for the memory path issues no products.
+    const auto multiply = [&](const Operands &o, int part, Operands &coming, int from, int to) {
 #pragma unroll
-      for (int p = 0; p < kBlocks; ++p)
+      for (int p = 0; p < kBlocks; ++p) {
+        fetch(part, p, coming);
+        load(from + (to - from) * p / kBlocks, from + (to - from) * (p + 1) / kBlocks);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
           acc[p][q] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[p], o.x[q], acc[p][q], 0, 0, 0);
-      if constexpr (Q == 4) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // an LDS read, then two products
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     };
-    const __amdgpu_buffer_rsrc_t next_x = rows_of(next), next_w = channels_of(next);
     Operands even, odd;
-    fetch(stage, 0, even);
+#pragma unroll
+    for (int p = 0; p < kBlocks; ++p) fetch(0, p, even);
     for (int s = 0; s < steps; ++s) {
-      int step = s + 1;
-      if (step == steps) {  // the next unit's first step
-        step = 0, bx = next_x, bw = next_w;
-        load_scales(next, turn < 2 ? turn + 1 : 0);
-      }
-      const uint32_t to = place + (stage ^ 1) * kStageBytes;
-      load(bx, step, to);
-      fetch(stage, 1, odd);
-      multiply(even);
-      load(bw, step, to + kOperandBytes);
-      ahead(s + 3 < steps ? bx : next_x, s + 3 < steps ? s + 3 : s + 3 - steps);
-      ahead(s + 3 < steps ? bw : next_w, s + 3 < steps ? s + 3 : s + 3 - steps);
-      fetch(stage, 2, even);
-      multiply(odd);
-      fetch(stage, 3, odd);
-      multiply(even);
-      // Before a step's operands are read its loads have to be there (the two that only reach L2
-      // may be on their way: loads return in order), and every wave has read the step before it,
-      // whose place the next loads take.
+      multiply(even, 1, odd, kIssued[0], kIssued[1]);
+      multiply(odd, 2, even, kIssued[1], kIssued[2]);
+      multiply(even, 3, odd, kIssued[2], kIssued[3]);
+      // Before the next step's operands are read its loads have to be there, and every wave has read
+      // this step's, whose place the loads of the step behind it take.
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
+      advance(stage);
       stage ^= 1;
-      fetch(stage, 0, even);  // behind the last step: not used
-      multiply(odd);
+      multiply(odd, 0, even, 0, kIssued[0]);  // behind the last step: operands that are not used
     }
     // Results leave through LDS as whole lines of 32 rows.
     char *const mine = lines + wave * kBlock * kStrideOut;
@@ -292,16 +289,12 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
       }
     }
   };
-  for (;;) {
-    const bool more = u + groups < u1;
-    if (more) next = locate(u + groups, unit.e);
-    else next.rows = next.cols = 0;
+  for (; u < u1; u += groups, turn = turn < 2 ? turn + 1 : 0) {
+    unit = locate(u, unit.e);
     if (unit.rows > 6 * kBlock) tile(std::integral_constant<int, 4>());
     else if (unit.rows > 4 * kBlock) tile(std::integral_constant<int, 3>());
     else if (unit.rows > 2 * kBlock) tile(std::integral_constant<int, 2>());
     else tile(std::integral_constant<int, 1>());
-    if (!more) break;
-    unit = next, u += groups, turn = turn < 2 ? turn + 1 : 0;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads into this workgroup's LDS
 }
