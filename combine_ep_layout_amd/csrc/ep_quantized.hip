@@ -194,10 +194,7 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   };
   // A step's loads that are issued by the ends of the last part of the second step before it, and of
   // the parts of the step before it.
-#ifndef ISSUED
-#define ISSUED 6, 11, 16, 16
-#endif
-  constexpr int kIssued[4] = {ISSUED};
+  constexpr int kIssued[4] = {8, 16, 16, 16};
   int stage = 0, turn = 0;  // of the step, of the unit
   load_scales(ahead.unit, 0);
   load(0, 2 * kLoads);
