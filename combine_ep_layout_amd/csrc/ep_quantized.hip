@@ -60,6 +60,17 @@ constexpr int kSide = 256, kBlock = 32, kBlocks = 4;
 constexpr int kOperandBytes = kSide * kStep, kStageBytes = 2 * kOperandBytes;  // of a step: x, then w
 constexpr int kLineOut = 128, kStrideOut = kLineOut + 16;  // results leave by lines of 32 rows
 
+// The rows of expert e inside the buffer: their number, and the first in `begin`.
+__device__ __forceinline__ int span_of(const QuantizedMatmulArgs &a, int e, int &begin) {
+  if (a.counts == nullptr) {
+    begin = 0;
+    return (int)a.capacity;
+  }
+  begin = a.offsets[e];
+  const int n = clip_span(begin, a.counts[e], a.capacity);
+  return n > 0 ? n : 0;
+}
+
 // Tiles of the experts before e, for every e: a workgroup's own prefix sums in LDS.
 template <class F>
 __device__ __forceinline__ void prefix_tiles(int *before, int *wave_sums, int E, F tiles) {
@@ -87,8 +98,21 @@ struct Unit {
   int64_t first;  // row of the buffer
 };
 
+// The expert whose tiles unit v is among, not before `from`: most often that one or the next.
+__device__ __forceinline__ int expert_of(const int *before, int E, int v, int from) {
+  if (from + 1 >= E || __builtin_amdgcn_readfirstlane(before[from + 1]) > v) return from;
+  int lo = from + 1, hi = E;  // before[lo] <= v < before[hi]
+  if (lo + 1 < E && __builtin_amdgcn_readfirstlane(before[lo + 1]) > v) return lo;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__builtin_amdgcn_readfirstlane(before[mid]) <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 template <bool FP32>
-__global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a) {
+__global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const QuantizedMatmulArgs a, int few) {
   constexpr int kLoads = kSide / 8 / kWaves;  // of a wave per operand and step: a line of 8 rows each
   constexpr int kElt = FP32 ? 4 : 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
@@ -101,18 +125,10 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   const int wm = (wave & 1) * kBlock, wn = (wave >> 1) * (kSide / 2);
   const int N = a.N, K = a.K;
   const int tiles_n = (N + kSide - 1) / kSide, steps = (K + kStep - 1) / kStep;
-  const auto span = [&](int e, int &begin) {
-    if (a.counts == nullptr) {
-      begin = 0;
-      return (int)a.capacity;
-    }
-    begin = a.offsets[e];
-    const int n = clip_span(begin, a.counts[e], a.capacity);
-    return n > 0 ? n : 0;
-  };
   prefix_tiles(before, wave_sums, a.E, [&](int e) {
     int b;
-    return (span(e, b) + kSide - 1) / kSide * tiles_n;
+    const int n = span_of(a, e, b);
+    return n > few ? (n + kSide - 1) / kSide * tiles_n : 0;
   });
   const int units = __builtin_amdgcn_readfirstlane(before[a.E]);
   // Workgroup b runs on XCD b % 8: each XCD takes a run of consecutive units.
@@ -123,10 +139,9 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   if (u >= u1) return;
   // Unit v, for an expert that is not before `from`.
   const auto locate = [&](int v, int from) {
-    Unit t{from, 0, 0, 0, 0};
-    while (t.e + 1 < a.E && __builtin_amdgcn_readfirstlane(before[t.e + 1]) <= v) ++t.e;
+    Unit t{expert_of(before, a.E, v, from), 0, 0, 0, 0};
     int begin;
-    const int count = __builtin_amdgcn_readfirstlane(span(t.e, begin)), tiles_m = (count + kSide - 1) / kSide;
+    const int count = __builtin_amdgcn_readfirstlane(span_of(a, t.e, begin)), tiles_m = (count + kSide - 1) / kSide;
     const int i = v - __builtin_amdgcn_readfirstlane(before[t.e]);
     if (i < 0 || i >= tiles_m * tiles_n) return t;  // spans that overlap so often that their tiles pass 2^31
     constexpr int kTall = 4;  // row tiles side by side before the next column tile
@@ -157,21 +172,12 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
     touch(buffer_of(uniform((const char *)(a.w_scales + (int64_t)t.e * N + t.n0)), (int64_t)t.cols * 4), threadIdx.x * 4u,
           lds_at(scales[turn][1] + wave * kWave));
   };
-  int e0 = 0;
-  {
-    int hi = a.E;
-    while (hi - e0 > 1) {
-      const int mid = (e0 + hi) / 2;
-      if (__builtin_amdgcn_readfirstlane(before[mid]) <= u) e0 = mid;
-      else hi = mid;
-    }
-  }
   // What is loaded next: a step of a unit that may be ahead of the one that is multiplied.
   struct {
     Unit unit;
     int u, step, turn;
     uint32_t place;
-  } ahead{locate(u, e0), u, 0, 0, place};
+  } ahead{locate(u, 0), u, 0, 0, place};
   __amdgpu_buffer_rsrc_t ahead_x = rows_of(ahead.unit), ahead_w = channels_of(ahead.unit);
   const auto advance = [&](int to) {
     ahead.place = place + to * kStageBytes;
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   advance(1);
   load(0, kIssued[0]);
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kIssued[0]) : "memory");
-  Unit unit{e0, 0, 0, 0, 0};
+  Unit unit{0, 0, 0, 0, 0};
 
   const auto tile = [&](auto row_blocks) {
     constexpr int Q = decltype(row_blocks)::value;  // of every wave
@@ -296,15 +302,199 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads into this workgroup's LDS
 }
 
+// Few rows: a workgroup takes RT * 16 channels of an expert with up to MT * 16 rows, its four waves a
+// quarter of the long axis each, through a ring of LDS of their own that no other wave waits for. The
+// rings run on from unit to unit; a unit's sums meet in LDS (integers: in any order).
+constexpr int kFew = 32;              // rows
+constexpr int kRingBytes = 36 * 1024;  // of a wave
+constexpr int kScaleSlots = 9;         // units whose scales may be in LDS: one more than a ring has steps, and the one before
+struct FewLds {
+  char ring[kWaves][kRingBytes];
+  int sums[kFew * 64];
+  float scales[kScaleSlots][64 + kFew];
+  int before[EP_MAX_EXPERTS + 1];
+  int wave_sums[kWaves];
+};
+
+template <bool FP32, int RT, int MT>
+__device__ __forceinline__ void few_rows(const QuantizedMatmulArgs &a, FewLds &lds) {
+  constexpr int kChannels = RT * 16, kRows = MT * 16, kLoads = 2 * (RT + MT);
+  constexpr int kStepBytes = (kChannels + kRows) * kStep;
+  constexpr int kDeep = kRingBytes / kStepBytes < 8 ? kRingBytes / kStepBytes : 8;  // steps in a ring
+  static_assert(kDeep < kScaleSlots && (kDeep - 1) * kLoads < 60, "units in flight, and what a wait can count");
+  const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int N = a.N, K = a.K;
+  const int tiles_n = (N + kChannels - 1) / kChannels, steps = (K + kStep - 1) / kStep;
+  prefix_tiles(lds.before, lds.wave_sums, a.E, [&](int e) {
+    int b;
+    const int n = span_of(a, e, b);
+    return n > 0 && n <= kFew ? tiles_n : 0;
+  });
+  const int units = __builtin_amdgcn_readfirstlane(lds.before[a.E]);
+  const int s0 = steps * wave / kWaves, own = steps * (wave + 1) / kWaves - s0;  // the last wave has a step at least
+  struct Unit {
+    int e, rows, n0;
+    int64_t first;
+  };
+  const auto locate = [&](int v, int from) {
+    Unit t{expert_of(lds.before, a.E, v, from), 0, 0, 0};
+    int begin;
+    t.rows = __builtin_amdgcn_readfirstlane(span_of(a, t.e, begin));
+    t.first = __builtin_amdgcn_readfirstlane(begin);
+    t.n0 = (v - __builtin_amdgcn_readfirstlane(lds.before[t.e])) * kChannels;
+    if (t.n0 < 0 || t.n0 >= N || t.rows > kFew) t.rows = 0, t.n0 = 0;  // never for spans of a layout
+    return t;
+  };
+  const auto channels = [&](const Unit &t) { return t.rows == 0 ? 0 : (N - t.n0 < kChannels ? N - t.n0 : kChannels); };
+  const int piece = ((lane & 7) ^ (lane >> 4)) * 16;
+  const uint32_t off = (uint32_t)(lane >> 3) * (uint32_t)K;
+  const uint32_t ring = lds_at(lds.ring[wave]);
+  // What is loaded next: a step of a unit ahead of the one that is multiplied.
+  int au = blockIdx.x, as = 0, aslot = 0, aturn = 0;
+  Unit at = locate(au < units ? au : 0, 0);
+  if (au >= units) at.rows = 0;
+  const auto rows_of = [&](const Unit &t) { return buffer_of(uniform((const char *)a.x + t.first * K), (int64_t)t.rows * K); };
+  const auto channels_of = [&](const Unit &t) {
+    return buffer_of(uniform((const char *)a.w + ((int64_t)t.e * N + t.n0) * K), (int64_t)channels(t) * K);
+  };
+  __amdgpu_buffer_rsrc_t bx = rows_of(at), bw = channels_of(at);
+  const auto load = [&] {
+    if (as == 0 && wave == kWaves - 1) {  // a unit's scales, ahead of its steps
+      touch(buffer_of(uniform((const char *)(a.w_scales + (int64_t)at.e * N + at.n0)), (int64_t)channels(at) * 4), lane * 4u,
+            lds_at(lds.scales[aturn]));
+      const __amdgpu_buffer_rsrc_t bs =
+          buffer_of(uniform((const char *)(a.x_scales + at.first * a.x_scale_cols)), (int64_t)at.rows * a.x_scale_cols * 4);
+      const uint32_t to = lds_at(lds.scales[aturn] + 64);
+      if (lane < kFew) touch(bs, lane * (uint32_t)a.x_scale_cols * 4u, to);  // there is no room for 64
+    }
+    const uint32_t to = ring + aslot * kStepBytes;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t k = (s0 + as) * kStep + (i & 1 ? piece ^ 64 : piece);
+      const int block = i < 2 * RT ? i : i - 2 * RT;
+      load_to_lds(i < 2 * RT ? bw : bx, off + (uint32_t)(block * 8) * (uint32_t)K + (k < (uint32_t)K ? k : kBehind), to + i * 1024);
+    }
+    aslot = aslot + 1 < kDeep ? aslot + 1 : 0;
+    if (++as == own) {
+      as = 0, au += gridDim.x, aturn = aturn + 1 < kScaleSlots ? aturn + 1 : 0;
+      if (au < units) at = locate(au, at.e);
+      else at.rows = 0;
+      bx = rows_of(at), bw = channels_of(at);
+    }
+  };
+  if (own > 0)
+    for (int i = 0; i < kDeep - 1; ++i) load();
+  for (int i = threadIdx.x; i < kRows * kChannels; i += kThreads) lds.sums[i] = 0;
+  int slot = 0, turn = 0, e = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x, turn = turn + 1 < kScaleSlots ? turn + 1 : 0) {
+    i32x4 acc[RT][MT];
+#pragma unroll
+    for (int p = 0; p < RT; ++p)
+#pragma unroll
+      for (int q = 0; q < MT; ++q) acc[p][q] = i32x4{0, 0, 0, 0};
+    for (int s = 0; s < own; ++s) {
+      // This step's loads are there (those behind it may be on their way: loads return in order), and
+      // the last step's operands have been read, whose place the next loads take.
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kDeep - 2) * kLoads) : "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      load();
+      const char *const from = lds.ring[wave] + slot * kStepBytes + r16 * kStep;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int p16 = ((4 * j + g) ^ (r16 >> 1)) * 16;
+        i32x4 w[RT], x[MT];
+#pragma unroll
+        for (int p = 0; p < RT; ++p) w[p] = *(const i32x4 *)(from + p * 16 * kStep + p16);
+#pragma unroll
+        for (int q = 0; q < MT; ++q) x[q] = *(const i32x4 *)(from + (kChannels + q * 16) * kStep + p16);
+#pragma unroll
+        for (int p = 0; p < RT; ++p)
+#pragma unroll
+          for (int q = 0; q < MT; ++q) acc[p][q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[p], x[q], acc[p][q], 0, 0, 0);
+      }
+      slot = slot + 1 < kDeep ? slot + 1 : 0;
+    }
+    const Unit t = locate(u, e);
+    e = t.e;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the last unit's sums have been read and cleared
+#pragma unroll
+    for (int p = 0; p < RT; ++p)
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) atomicAdd(&lds.sums[(q * 16 + r16) * kChannels + p * 16 + g * 4 + i], acc[p][q][i]);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    constexpr int kLanes = kChannels / 4;  // four channels a thread
+#pragma unroll
+    for (int first = 0; first < kRows; first += kThreads / kLanes) {
+      const int row = first + threadIdx.x / kLanes, c = threadIdx.x % kLanes * 4;
+      if (row >= kRows) continue;
+      i32x4 *const from = (i32x4 *)(lds.sums + row * kChannels + c);
+      const i32x4 sum = *from;
+      *from = i32x4{0, 0, 0, 0};
+      if (row >= t.rows || t.n0 + c >= N) continue;
+      const float sx = lds.scales[turn][64 + row];
+      const f32x4 sw = *(const f32x4 *)(lds.scales[turn] + c);
+      f32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * sx * sw[i];
+      const int64_t to = (t.first + row) * N + t.n0 + c;
+      if constexpr (FP32) *(f32x4 *)((float *)a.y + to) = v;
+      else *(u32x2 *)((uint16_t *)a.y + to) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads into this workgroup's LDS
+}
+
+template <bool FP32>
+__global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_few(const QuantizedMatmulArgs a, int enough) {
+  __shared__ __attribute__((aligned(1024))) FewLds lds;
+  // Experts with few rows, and the most rows of one.
+  int active = 0, most = 0;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    int b;
+    const int n = span_of(a, e, b);
+    if (n > 0 && n <= kFew) ++active, most = n > most ? n : most;
+  }
+  if (threadIdx.x < 2) lds.sums[threadIdx.x] = 0;
+  __syncthreads();
+  if (active > 0) {
+    atomicAdd(&lds.sums[0], active);
+    atomicMax(&lds.sums[1], most);
+  }
+  __syncthreads();
+  active = __builtin_amdgcn_readfirstlane(lds.sums[0]), most = __builtin_amdgcn_readfirstlane(lds.sums[1]);
+  __syncthreads();
+  if (active == 0) return;
+  if ((int64_t)active * ((a.N + 63) / 64) >= enough) {
+    if (most <= 16) few_rows<FP32, 4, 1>(a, lds);
+    else few_rows<FP32, 4, 2>(a, lds);
+  } else {
+    if (most <= 16) few_rows<FP32, 1, 1>(a, lds);
+    else few_rows<FP32, 1, 2>(a, lds);
+  }
+}
+
 }  // namespace
 
 int launch_quantized_matmul(const QuantizedMatmulArgs &a) {
   if (a.capacity == 0) return 0;
   const int cap = stream_workgroup_limit(a.stream);
   const unsigned grid = cap > 0 && cap < 256 ? cap : 256;
-  if (a.fp32) ep_quantized_matmul_tiles<true><<<grid, kThreads, 0, a.stream>>>(a);
-  else ep_quantized_matmul_tiles<false><<<grid, kThreads, 0, a.stream>>>(a);
-  return launch_status();
+  const auto run = [&](auto kernel, int n) {
+    kernel<<<grid, kThreads, 0, a.stream>>>(a, n);
+    return launch_status();
+  };
+  // Experts with few rows, then those with more: a buffer of few rows has none of them, and one expert
+  // without routing arrays is of one kind.
+  if (a.counts != nullptr || a.capacity <= kFew) {
+    const int enough = 2 * (int)grid;
+    const int rc = a.fp32 ? run(ep_quantized_matmul_few<true>, enough) : run(ep_quantized_matmul_few<false>, enough);
+    if (rc != 0 || a.capacity <= kFew) return rc;
+  }
+  return a.fp32 ? run(ep_quantized_matmul_tiles<true>, kFew) : run(ep_quantized_matmul_tiles<false>, kFew);
 }
 
 }  // namespace ep
