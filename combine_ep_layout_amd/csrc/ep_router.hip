@@ -21,20 +21,47 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMaxThreads = 1024;
 constexpr float kInf = __builtin_inff();
 
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int d = 1; d < L; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+// Reductions over a row's L lanes (16 or 64; the same result in each of them). Within 16 lanes by DPP
+// rotations. Every lane of the wave takes part: nothing here may be called by some lanes only.
+template <int N>
+__device__ __forceinline__ int rotate(int v) {  // by N within 16 lanes
+  constexpr int kRowRor = 0x120;
+  return __builtin_amdgcn_update_dpp(0, v, kRowRor + N, 0xF, 0xF, false);
+}
+template <int L, class F>
+__device__ __forceinline__ int over_lanes(int v, F f) {
+  v = f(v, rotate<8>(v));
+  v = f(v, rotate<4>(v));
+  v = f(v, rotate<2>(v));
+  v = f(v, rotate<1>(v));
+  if constexpr (L == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
   return v;
 }
 template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  return __int_as_float(over_lanes<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+  }));
+}
+template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d);
-  return v;
+  return __int_as_float(over_lanes<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return (uint32_t)over_lanes<L>((int)v, [](int a, int b) { return (uint32_t)a > (uint32_t)b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ bool lanes_any(bool p) {
+  return lanes_max<L>((uint32_t)p) != 0;
 }
 
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -90,10 +117,12 @@ __device__ __forceinline__ float load_one(const void *x, int64_t at) {
   else return bf16_value(((const uint16_t *)x)[at]);
 }
 
-// exp(l - ref) for softmax; for sigmoids s(l) * exp(-ref), ref = min(the largest l, 0).
+// exp(l - ref) for softmax; for sigmoids s(l) * exp(-ref), ref = min(the largest l, 0). Exponentials by
+// the exp2 instruction, quotients by the reciprocal: (|l - ref| + 8) * 2^-23 relative at most.
 __device__ __forceinline__ float term(bool sigmoid, float l, float ref) {
   if (!sigmoid) return __expf(l - ref);
-  return l >= 0.f ? 1.0f / (1.0f + __expf(-l)) : __expf(l - ref) / (1.0f + __expf(l));
+  const float small = __expf(-fabsf(l)), by = __builtin_amdgcn_rcpf(1.0f + small);
+  return l >= 0.f ? by : __expf(l - ref) * by;
 }
 __device__ __forceinline__ float reference(bool sigmoid, float top) {
   if (top == -kInf) return 0.f;  // nothing is above -infinity: every term is 0
@@ -120,43 +149,120 @@ struct Slots {  // partial sums per (tile + sequence), then per sequence
   double *seq_balance, *seq_z;  // [S]
 };
 
-// One row's K ids, by descending key and ascending id; lane i of the L keeps those of places i,
-// i + L, ...: ids[b] is place b * L + i.
-template <int L, int V, int KB>
-__device__ __forceinline__ void choose(double (&key)[V], int i, int K, int (&ids)[KB]) {
-#pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    ids[b] = -1;
-    for (int k = b * L; k < K && k < (b + 1) * L; ++k) {
-      double best = -(double)kInf;
-      int at = 1 << 30;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (key[j] > best) best = key[j], at = column<L, V>(i, j);
-#pragma unroll
-      for (int d = 1; d < L; d *= 2) {
-        const double other = __shfl_xor(best, d);
-        const int o = __shfl_xor(at, d);
-        if (other > best || (other == best && o < at)) best = other, at = o;
-      }
-      if (k % L == i && best > -(double)kInf) ids[b] = at;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (column<L, V>(i, j) == at) key[j] = -(double)kInf;
-    }
-  }
+// The order of binary32 numbers as that of integers (-0 has to be +0), and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// Choice of a row's K largest keys, ties by ascending column.
+//
+// Fast: a key's upper bits and its column (descending) in one 31-bit number, so that a maximum is one integer
+// instruction and names its column; x - m, as an unsigned number, puts what is still below the last
+// maximum m on top. bf16 logits fit whole. Of binary32 keys the lower bits are lost: then K + 2
+// candidates are taken and ranked by their whole keys, and the choice stands if what was
+// left out lies below the K-th whatever its lower bits are, and, for score + bias, if neighbours differ
+// by more than the keys' own rounding errors.
+// Exact: binary64 keys, one maximum at a time; for the rows where the fast way cannot tell, and for more
+// candidates than lanes.
+template <int L, int V>
+struct Chooser {
+  static constexpr int kColumnBits = (L * V <= 16 ? 4 : L * V <= 32 ? 5 : L * V <= 64 ? 6 : L * V <= 128 ? 7 : L * V <= 256 ? 8 : L * V <= 512 ? 9 : 10);
+  static constexpr uint32_t kColumns = (1u << kColumnBits) - 1;
+  static constexpr int kLost = kColumnBits + 1;  // lower bits of a key
+
+  // The packed number of a key; 0: not to be chosen.
+  static __device__ __forceinline__ uint32_t pack(float key, int column) {
+    const uint32_t u = ordered(key + 0.0f) >> kLost << kColumnBits | (kColumns - (uint32_t)column);
+    return key > -kInf ? u : 0u;
+  }
+  // The largest C packed numbers: lane k has the k-th (0: none).
+  static __device__ __forceinline__ uint32_t largest(const uint32_t (&x)[V], int C, int i) {
+    uint32_t last = 0x80000000u, mine = 0;
+    for (int k = 0; k < C; ++k) {
+      uint32_t best = x[0] - last;
+#pragma unroll
+      for (int j = 1; j < V; ++j) {
+        const uint32_t t = x[j] - last;
+        best = t > best ? t : best;
+      }
+      best = lanes_max<L>(best) + last;
+      if (k == i) mine = best;
+      last = best > 1 ? best : 1;
+    }
+    return mine;
+  }
+  static __device__ __forceinline__ int column_of(uint32_t packed) { return (int)(kColumns - (packed & kColumns)); }
+  // A number that no key with this packed number exceeds.
+  static __device__ __forceinline__ float at_most(uint32_t packed) {
+    return unordered(packed >> kColumnBits << kLost | ((1u << kLost) - 1));
+  }
+
+  // Rank of this lane's (key, column) among the row's lanes, and whether another key is within `near`.
+  static __device__ __forceinline__ int rank(float key, int column, int C, float near, bool &close) {
+    int r = 0;
+    const auto against = [&](float k, int c) {
+      r += k > key || (k == key && c < column);
+      close |= fabsf(k - key) <= near && c != column;
+    };
+    if constexpr (L == 16) {
+#define EP_AGAINST(N) against(__int_as_float(rotate<N>(__float_as_int(key))), rotate<N>(column));
+      EP_AGAINST(1) EP_AGAINST(2) EP_AGAINST(3) EP_AGAINST(4) EP_AGAINST(5) EP_AGAINST(6) EP_AGAINST(7) EP_AGAINST(8)
+      EP_AGAINST(9) EP_AGAINST(10) EP_AGAINST(11) EP_AGAINST(12) EP_AGAINST(13) EP_AGAINST(14) EP_AGAINST(15)
+#undef EP_AGAINST
+    } else {
+      for (int c = 0; c < C; ++c) against(read_lane(key, c), read_lane(column, c));
+    }
+    return r;
+  }
+
+  // Exact: ids[b] of lane i is place b * L + i (-1: none left).
+  static __device__ __forceinline__ void exactly(double (&key)[V], int i, int K, int (&ids)[64 / L]) {
+#pragma unroll
+    for (int b = 0; b < 64 / L; ++b) {
+      ids[b] = -1;
+      for (int k = b * L; k < K && k < (b + 1) * L; ++k) {
+        double best = -(double)kInf;
+        int at = 1 << 30;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (key[j] > best) best = key[j], at = column<L, V>(i, j);
+#pragma unroll
+        for (int d = 1; d < L; d *= 2) {
+          const double other = __shfl_xor(best, d);
+          const int o = __shfl_xor(at, d);
+          if (other > best || (other == best && o < at)) best = other, at = o;
+        }
+        if (k % L == i && best > -(double)kInf) ids[b] = at;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (column<L, V>(i, j) == at) key[j] = -(double)kInf;
+      }
+    }
+  }
+};
+
 template <bool FP32, int L, int V>
-__global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
-                                                           Slots out) {
-  constexpr int KB = 64 / L, kGroups = kThreads / L;
-  __shared__ float sums[kGroups * L * V];
+__global__ __launch_bounds__(kMaxThreads) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
+                                                              Slots out) {
+  using Choice = Chooser<L, V>;
+  constexpr int KB = 64 / L, kWaveRows = kWave / L, kWaves = kMaxThreads / kWave;
+  __shared__ float sums[kWaves][L * V];
   __shared__ int hits[L * V];
-  __shared__ float zs[kGroups];
-  __shared__ int taken;
-  const int i = threadIdx.x % L, group = threadIdx.x / L, E = a.E, K = a.K;
+  __shared__ float zs[kWaves * kWaveRows];
+  __shared__ int taken[kWaves * kWaveRows];
+  const int i = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L, E = a.E, K = a.K;
   const bool stats = a.counts != nullptr;
+  const bool packed_whole = !FP32 && a.bias == nullptr;  // no key bits are lost
+  const int candidates = packed_whole ? K : (K + 2 < E ? K + 2 : E);
+  const bool fast = candidates <= L;
+  const bool all_terms = stats || a.bias != nullptr || !(a.normalize || a.sigmoid);
+  float bias[V];  // of this lane's columns
+#pragma unroll
+  for (int j = 0; j < V; ++j) bias[j] = a.bias != nullptr && column<L, V>(i, j) < E ? a.bias[column<L, V>(i, j)] : 0.f;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int last = a.T - tile * tile_rows < tile_rows ? a.T : (tile + 1) * tile_rows;
     for (int pos = tile * tile_rows; pos < last;) {
@@ -167,124 +273,176 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
       }
       const bool inside = stats && s >= 0 && s < a.S;
       float acc[V], z = 0.f;
+      int count = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = 0.f;
       if (inside) {
-        for (int c = threadIdx.x; c < E; c += kThreads) hits[c] = 0;
-        if (threadIdx.x == 0) taken = 0;
+        for (int c = threadIdx.x; c < E; c += blockDim.x) hits[c] = 0;
         __syncthreads();
       }
-      for (int first = pos; first < end; first += kGroups) {
+      for (int first = pos; first < end; first += groups) {
         const int row = first + group;
-        const bool on = row < end && (a.mask == nullptr || a.mask[row < end ? row : pos] != 0);
-        const bool there = row < end;
+        const bool there = row < end, on = there && (a.mask == nullptr || a.mask[there ? row : pos] != 0);
         float v[V];
         load_row<FP32, L, V>(a.logits, row, E, i, on, v);
-        float top = -kInf;
+        float top = -kInf, total = 0.f, ref = 0.f;
+        float e[V];
+        if (all_terms) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
-        top = lanes_max<L>(top);
-        const float ref = reference(a.sigmoid, top);
-        float e[V], total = 0.f;
+          for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
+          top = lanes_max<L>(top);
+          ref = reference(a.sigmoid, top);
 #pragma unroll
-        for (int j = 0; j < V; ++j) e[j] = term(a.sigmoid, v[j], ref), total += e[j];
-        total = lanes_sum<L>(total);
-        int ids[KB];
+          for (int j = 0; j < V; ++j) e[j] = term(a.sigmoid, v[j], ref), total += e[j];
+          total = lanes_sum<L>(total);
+        }
+        int ids[KB], places[KB];  // of this lane
+#pragma unroll
+        for (int b = 0; b < KB; ++b) places[b] = b * L + i, ids[b] = -1;
         if (!a.given) {
-          double key[V];
-          if (a.bias == nullptr) {
+          const float back = a.sigmoid ? (ref < 0.f ? __expf(ref) : 1.0f) : (total == 0.f ? 0.f : 1.0f / total);
+          const auto key_of = [&](int j) {
+            if (a.bias == nullptr) return v[j];
+            return v[j] > -kInf ? e[j] * back + bias[j] : -kInf;
+          };
+          bool unsure = !fast;
+          if (fast) {
+            uint32_t x[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) key[j] = v[j];
-          } else {
-            double sum = 0.0;
-            const double m = ref;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              key[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)v[j])) : exp((double)v[j] - m);
-              sum += key[j];
-            }
-#pragma unroll
-            for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const int c = column<L, V>(i, j);
-              const double bias = c < E ? a.bias[c] : 0.f;
-              key[j] = v[j] == -kInf ? -(double)kInf : (a.sigmoid ? key[j] : key[j] / sum) + bias;
+            for (int j = 0; j < V; ++j) x[j] = Choice::pack(key_of(j), column<L, V>(i, j));
+            const uint32_t mine = Choice::largest(x, candidates, i);
+            const bool valid = mine != 0 && i < candidates;
+            ids[0] = valid ? Choice::column_of(mine) : -1;
+            if (!packed_whole) {
+              float key = -kInf, near = -1.0f;
+              if (valid) {
+                key = load_one<FP32>(a.logits, (int64_t)row * E + ids[0]);
+                if (a.bias != nullptr) {
+                  // errors of scores: 16 * 2^-23 for sigmoids; 128 * 2^-23 of the largest probability
+                  const float most = fabsf(Choice::at_most(mine));
+                  near = (a.sigmoid ? 0x1p-19f : 0x1p-16f * back) + 0x1p-21f * most;
+                  key = term(a.sigmoid, key, ref) * back + a.bias[ids[0]];
+                }
+              }
+              bool close = false;
+              places[0] = Choice::rank(key, valid ? ids[0] : E + i, candidates, near, close);
+              // what was left out lies below the last candidate's packed number
+              const uint32_t left = (uint32_t)__shfl((int)mine, (int)(threadIdx.x & (kWave - 1)) / L * L + candidates - 1);
+              const bool rest = candidates < E && left != 0;
+              unsure = valid && ((close && places[0] <= K) || (rest && places[0] == K - 1 && !(key > Choice::at_most(left) + fmaxf(near, 0.f))));
+              if (places[0] >= K) ids[0] = -1;
             }
           }
-          choose<L, V, KB>(key, i, K, ids);
+          unsure = lanes_any<L>(unsure && there);
+          if (ballot(unsure) != 0) {
+            double key[V];
+            double sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              key[j] = v[j];
+              if (a.bias != nullptr) {
+                key[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)v[j])) : exp((double)v[j] - (double)ref);
+                sum += key[j];
+              }
+            }
+            if (a.bias != nullptr) {
+#pragma unroll
+              for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
+#pragma unroll
+              for (int j = 0; j < V; ++j)
+                key[j] = v[j] > -kInf ? (a.sigmoid ? key[j] : key[j] / sum) + (double)bias[j] : -(double)kInf;
+            }
+            int exact[KB];
+            Choice::exactly(key, i, K, exact);
+            if (unsure) {
+#pragma unroll
+              for (int b = 0; b < KB; ++b) ids[b] = exact[b], places[b] = b * L + i;
+            }
+          }
         } else {
 #pragma unroll
           for (int b = 0; b < KB; ++b) {
             const int k = b * L + i;
-            ids[b] = on && k < K ? a.idx[(int64_t)row * K + k] : -1;
+            if (on && k < K) ids[b] = a.idx[(int64_t)row * K + k];
             if ((uint32_t)ids[b] >= (uint32_t)E) ids[b] = -1;
           }
         }
         // weights, from the chosen logits
-        float l[KB], most = -kInf;
-        int any = 0;
+        float l[KB], w[KB], most = -kInf;
+        bool any = false;
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
+          if (ids[b] >= 0 && !there) ids[b] = -1;
           l[b] = ids[b] >= 0 ? load_one<FP32>(a.logits, (int64_t)row * E + ids[b]) : -kInf;
           most = fmaxf(most, l[b]);
           any |= ids[b] >= 0;
         }
-        any = lanes_max<L>((float)any) > 0.f;
-        if (there && (a.weights != nullptr || !a.given)) {
+        any = lanes_any<L>(any);
+        if (a.normalize) {
           const float from = reference(a.sigmoid, lanes_max<L>(most));
           float part = 0.f;
 #pragma unroll
-          for (int b = 0; b < KB; ++b)
-            if (ids[b] >= 0) part += term(a.sigmoid, l[b], from);
+          for (int b = 0; b < KB; ++b) {
+            w[b] = ids[b] >= 0 ? term(a.sigmoid, l[b], from) : 0.f;
+            part += w[b];
+          }
           part = lanes_sum<L>(part);
+          const float by = part == 0.f ? 0.f : a.scale / part;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) w[b] = ids[b] >= 0 ? w[b] * by : 0.f;
+        } else {
+          const float by = a.sigmoid ? a.scale : (total == 0.f ? 0.f : a.scale / total);
+#pragma unroll
+          for (int b = 0; b < KB; ++b) w[b] = ids[b] >= 0 ? by * term(a.sigmoid, l[b], a.sigmoid ? 0.f : ref) : 0.f;
+        }
+        if (there) {
 #pragma unroll
           for (int b = 0; b < KB; ++b) {
-            const int k = b * L + i;
-            if (k >= K) continue;
-            const int64_t at = (int64_t)row * K + k;
+            if (places[b] >= K) continue;
+            const int64_t at = (int64_t)row * K + places[b];
             if (!a.given) a.idx[at] = ids[b];
-            if (a.weights == nullptr) continue;
-            float w = 0.f;
-            if (ids[b] >= 0) {
-              if (a.normalize) w = part == 0.f ? 0.f : a.scale * (term(a.sigmoid, l[b], from) / part);
-              else if (a.sigmoid) w = a.scale * term(true, l[b], 0.f);
-              else w = total == 0.f ? 0.f : a.scale * (term(false, l[b], ref) / total);
-            }
-            a.weights[at] = w;
+            if (a.weights != nullptr) a.weights[at] = w[b];
           }
         }
-        if (inside && there && any) {
+        if (inside && any) {
           const float by = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
           for (int j = 0; j < V; ++j) acc[j] += e[j] * by;
-          if (i == 0) {
-            const float lse = top == -kInf ? 0.f : top + logf(total);
-            z += lse * lse;
-            atomicAdd(&taken, 1);
-          }
+          const float lse = top == -kInf ? 0.f : top + logf(total);
+          z += lse * lse;
+          ++count;
 #pragma unroll
           for (int b = 0; b < KB; ++b)
             if (ids[b] >= 0) atomicAdd(&hits[ids[b]], 1);
         }
       }
       if (inside) {
+        // a wave's rows first, then the waves in order
+        const int wave = threadIdx.x / kWave;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sums[group * (L * V) + column<L, V>(i, j)] = acc[j];
-        if (i == 0) zs[group] = z;
+        for (int j = 0; j < V; ++j) {
+          if constexpr (L == 16) {
+            acc[j] += __shfl_xor(acc[j], 16);
+            acc[j] += __shfl_xor(acc[j], 32);
+          }
+          if ((threadIdx.x & (kWave - 1)) < L) sums[wave][column<L, V>(i, j)] = acc[j];
+        }
+        if (i == 0) zs[group] = z, taken[group] = count;
         __syncthreads();
         const int64_t slot = tile + s;
-        for (int c = threadIdx.x; c < E; c += kThreads) {
+        const int waves = blockDim.x / kWave;
+        for (int c = threadIdx.x; c < E; c += blockDim.x) {
           float sum = 0.f;
-          for (int g = 0; g < kGroups; ++g) sum += sums[g * (L * V) + c];
+          for (int g = 0; g < waves; ++g) sum += sums[g][c];
           out.p[slot * E + c] = sum;
           out.counts[slot * E + c] = hits[c];
         }
         if (threadIdx.x == 0) {
           float sum = 0.f;
-          for (int g = 0; g < kGroups; ++g) sum += zs[g];
+          int n = 0;
+          for (int g = 0; g < groups; ++g) sum += zs[g], n += taken[g];
           out.z[slot] = sum;
-          out.tokens[slot] = taken;
+          out.tokens[slot] = n;
         }
         __syncthreads();
       }
@@ -293,65 +451,88 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
   }
 }
 
+// Sum over a workgroup, in a fixed order.
 __device__ __forceinline__ double block_sum(double v, double *lds) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
   __syncthreads();
-  lds[threadIdx.x] = v;
+  if ((threadIdx.x & (kWave - 1)) == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
-  for (int d = kThreads / 2; d > 0; d /= 2) {
-    if ((int)threadIdx.x < d) lds[threadIdx.x] += lds[threadIdx.x + d];
-    __syncthreads();
-  }
-  return lds[0];
+  double sum = 0.0;
+  for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += lds[w];
+  return sum;
 }
 
-// A sequence's slots: its counts, tokens and terms of the losses.
-__global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs a, int tile_rows, Slots in) {
-  __shared__ double lds[kThreads];
-  for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+__device__ __forceinline__ void write_losses(const RouterArgs &a, double balance, double z, double full, double n) {
+  a.seq_tokens[a.S] = (int)full, a.seq_tokens[a.S + 1] = (int)n;
+  if (a.balance != nullptr) *a.balance = full > 0 ? (float)(balance / full) : 0.f;
+  if (a.z != nullptr) *a.z = n > 0 ? (float)(z / n) : 0.f;
+}
+
+// A sequence's slots: its counts, tokens and terms of the losses; with `parts` workgroups a sequence, each
+// for some of the columns. A workgroup of `lanes` x (threads / lanes): columns by slots.
+__global__ __launch_bounds__(kMaxThreads) void ep_router_sequences(const RouterArgs a, int tile_rows, Slots in, int parts,
+                                                                   int lanes) {
+  __shared__ double lds[kMaxThreads / kWave];
+  __shared__ double sums[kMaxThreads];
+  __shared__ int hits[kMaxThreads];
+  const int rows = blockDim.x / lanes, r = threadIdx.x / lanes, i = threadIdx.x % lanes;
+  for (int u = blockIdx.x; u < a.S * parts; u += gridDim.x) {
+    const int s = u / parts, part = u % parts;
     int b = 0, e = a.T;
     if (a.seq != nullptr) {
       b = a.seq[s] < 0 ? 0 : a.seq[s];
       e = a.seq[s + 1] < a.T ? a.seq[s + 1] : a.T;
     }
     const int first = b < e ? b / tile_rows : 0, end = b < e ? (e - 1) / tile_rows + 1 : 0;
-    int n = 0;
-    double z = 0.0;
-    for (int t = first; t < end; ++t) n += in.tokens[t + s], z += in.z[t + s];
-    double sum = 0.0;
-    for (int c = threadIdx.x; c < a.E; c += kThreads) {
+    double tokens = 0.0, z = 0.0, sum = 0.0;
+    for (int t = first + threadIdx.x; t < end; t += blockDim.x) tokens += in.tokens[t + s], z += in.z[t + s];
+    const int c0 = part * lanes, step = parts * lanes;
+    for (int c = c0; c < a.E; c += step) {
       double p = 0.0;
       int hit = 0;
-      for (int t = first; t < end; ++t) {
-        const int64_t at = (int64_t)(t + s) * a.E + c;
-        p += in.p[at], hit += in.counts[at];
+      if (c + i < a.E) {
+#pragma unroll 4
+        for (int t = first + r; t < end; t += rows) {
+          const int64_t at = (int64_t)(t + s) * a.E + c + i;
+          p += in.p[at], hit += in.counts[at];
+        }
       }
-      a.counts[(int64_t)s * a.E + c] = hit;
-      sum += hit * p;
+      __syncthreads();
+      sums[threadIdx.x] = p, hits[threadIdx.x] = hit;
+      __syncthreads();
+      if (r == 0 && c + i < a.E) {
+        for (int k = 1; k < rows; ++k) p += sums[k * lanes + i], hit += hits[k * lanes + i];
+        a.counts[(int64_t)s * a.E + c + i] = hit;
+        sum += hit * p;
+      }
     }
     sum = block_sum(sum, lds);
+    tokens = block_sum(tokens, lds);
+    z = block_sum(z, lds);
     if (threadIdx.x == 0) {
-      a.seq_tokens[s] = n;
-      in.seq_balance[s] = n > 0 ? sum * a.E / ((double)a.K * n * n) : 0.0;
-      in.seq_z[s] = z;
+      const double n = tokens;
+      if (part == 0) a.seq_tokens[s] = (int)n;
+      sum = n > 0 ? sum * a.E / ((double)a.K * n * n) : 0.0;
+      if (a.S * parts == 1) {
+        write_losses(a, sum, z, n > 0, n);
+      } else {
+        in.seq_balance[u] = sum;
+        in.seq_z[u] = part == 0 ? z : 0.0;
+      }
     }
   }
 }
 
 // The losses from the sequences' terms.
-__global__ __launch_bounds__(kThreads) void ep_router_losses(const RouterArgs a, Slots in) {
-  __shared__ double lds[kThreads];
+__global__ __launch_bounds__(kThreads) void ep_router_losses(const RouterArgs a, Slots in, int parts) {
+  __shared__ double lds[kMaxThreads / kWave];
   double balance = 0.0, z = 0.0, full = 0.0, n = 0.0;
-  for (int s = threadIdx.x; s < a.S; s += kThreads) {
-    balance += in.seq_balance[s], z += in.seq_z[s];
-    n += a.seq_tokens[s], full += a.seq_tokens[s] > 0;
-  }
+  for (int s = threadIdx.x; s < a.S * parts; s += kThreads) balance += in.seq_balance[s], z += in.seq_z[s];
+  for (int s = threadIdx.x; s < a.S; s += kThreads) n += a.seq_tokens[s], full += a.seq_tokens[s] > 0;
   balance = block_sum(balance, lds), z = block_sum(z, lds);
   n = block_sum(n, lds), full = block_sum(full, lds);
-  if (threadIdx.x == 0) {
-    a.seq_tokens[a.S] = (int)full, a.seq_tokens[a.S + 1] = (int)n;
-    if (a.balance != nullptr) *a.balance = full > 0 ? (float)(balance / full) : 0.f;
-    if (a.z != nullptr) *a.z = n > 0 ? (float)(z / n) : 0.f;
-  }
+  if (threadIdx.x == 0) write_losses(a, balance, z, full, n);
 }
 
 template <bool FP32, int L, int V>
@@ -381,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
       most = fmaxf(most, l[b]);
       any |= ids[b] >= 0;
     }
-    any = lanes_max<L>((float)any) > 0.f;
+    any = lanes_any<L>(any);
     float top = -kInf;
 #pragma unroll
     for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
@@ -490,7 +671,15 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
   }
 }
 
-int tile_rows_of(int) { return 64; }
+// Tokens per tile and slot: 64, one or four per group of lanes of a workgroup; 256 where those make too many slots.
+int tile_rows_of(int T) { return T > 64 * 1024 ? 256 : 64; }
+
+// Workgroups for the slots of a sequence: several where there are too many for one.
+constexpr int kMaxParts = 16;
+int parts_of(const RouterArgs &a, int64_t tiles) {
+  if (a.S > 1 || tiles <= 64) return 1;
+  return kMaxParts;
+}
 
 int64_t slots_of(int T, int S) {
   const int rows = tile_rows_of(T);
@@ -515,7 +704,7 @@ int for_shape(int E, F f) {
 
 size_t router_workspace(int T, int E, int S) {
   const int64_t slots = slots_of(T, S);
-  return (size_t)(2 * up(slots * E * 4) + 2 * up(slots * 4) + 2 * up((int64_t)S * 8));
+  return (size_t)(2 * up(slots * E * 4) + 2 * up(slots * 4) + 2 * up((int64_t)(S + kMaxParts) * 8));
 }
 
 int launch_router(const RouterArgs &a) {
@@ -530,23 +719,31 @@ int launch_router(const RouterArgs &a) {
       at += up(bytes);
       return p;
     };
-    w.seq_balance = (double *)take((int64_t)a.S * 8), w.seq_z = (double *)take((int64_t)a.S * 8);
+    w.seq_balance = (double *)take((int64_t)(a.S + kMaxParts) * 8), w.seq_z = (double *)take((int64_t)(a.S + kMaxParts) * 8);
     w.p = (float *)take(slots * a.E * 4), w.counts = (int *)take(slots * a.E * 4);
     w.z = (float *)take(slots * 4), w.tokens = (int *)take(slots * 4);
   }
   if (a.T > 0) {
-    const unsigned grid = (unsigned)(cap > 0 && cap < tiles ? cap : tiles);
     const int rc = for_shape(a.E, [&](auto l, auto v) {
-      if (a.fp32) ep_router_rows<true, decltype(l)::value, decltype(v)::value><<<grid, kThreads, 0, a.stream>>>(a, rows, tiles, w);
-      else ep_router_rows<false, decltype(l)::value, decltype(v)::value><<<grid, kThreads, 0, a.stream>>>(a, rows, tiles, w);
+      constexpr int L = decltype(l)::value, V = decltype(v)::value;
+      // With statistics a tile's workgroup is large, so that few slots are left; without, small.
+      const int threads = a.counts != nullptr ? (cap > 0 ? kThreads : kMaxThreads) : 64;
+      const int per = a.counts != nullptr ? rows : threads / L;
+      const int n = (a.T + per - 1) / per, most = cap > 0 ? cap : 1 << 20;
+      const unsigned grid = (unsigned)(n < most ? n : most);
+      if (a.fp32) ep_router_rows<true, L, V><<<grid, threads, 0, a.stream>>>(a, per, n, w);
+      else ep_router_rows<false, L, V><<<grid, threads, 0, a.stream>>>(a, per, n, w);
       return launch_status();
     });
     if (rc != 0) return rc;
   }
   if (a.counts == nullptr) return 0;
-  ep_router_sequences<<<(unsigned)(cap > 0 && cap < a.S ? cap : a.S), kThreads, 0, a.stream>>>(a, rows, w);
+  const int parts = parts_of(a, tiles);
+  const int lanes = parts > 1 ? 64 : (a.E <= 64 ? 64 : (a.E <= 128 ? 128 : 256)), units = a.S * parts;
+  ep_router_sequences<<<(unsigned)(cap > 0 && cap < units ? cap : units), kMaxThreads, 0, a.stream>>>(a, rows, w, parts, lanes);
   if (const int rc = launch_status()) return rc;
-  ep_router_losses<<<1, kThreads, 0, a.stream>>>(a, w);
+  if (units == 1) return 0;
+  ep_router_losses<<<1, kThreads, 0, a.stream>>>(a, w, parts);
   return launch_status();
 }
 
