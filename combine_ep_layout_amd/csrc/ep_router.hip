@@ -21,7 +21,7 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256, kMaxThreads = 1024;
+constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
 // Reductions over a row's L lanes (16 or 64; the same result in each of them). Within 16 lanes by DPP
@@ -146,7 +146,9 @@ struct Slots {  // partial sums per (tile + sequence), then per sequence
   int *counts;   // [slots, E]
   float *z;      // [slots]
   int *tokens;   // [slots]
-  double *seq_balance, *seq_z;  // [S]
+  double *balance;  // [S, parts]: terms of the balance loss
+  double *seq_z;    // [S]
+  unsigned *done;   // workgroups of the second launch that have left their terms
 };
 
 // The order of binary32 numbers as that of integers (-0 has to be +0), and back.
@@ -246,10 +248,10 @@ struct Chooser {
 };
 
 template <bool FP32, int L, int V>
-__global__ __launch_bounds__(kMaxThreads) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
+__global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
-  constexpr int KB = 64 / L, kWaveRows = kWave / L, kWaves = kMaxThreads / kWave;
+  constexpr int KB = 64 / L, kWaveRows = kWave / L, kWaves = kThreads / kWave;
   __shared__ float sums[kWaves][L * V];
   __shared__ int hits[L * V];
   __shared__ float zs[kWaves * kWaveRows];
@@ -263,6 +265,7 @@ __global__ __launch_bounds__(kMaxThreads) void ep_router_rows(const RouterArgs a
   float bias[V];  // of this lane's columns
 #pragma unroll
   for (int j = 0; j < V; ++j) bias[j] = a.bias != nullptr && column<L, V>(i, j) < E ? a.bias[column<L, V>(i, j)] : 0.f;
+  if (stats && blockIdx.x == 0 && threadIdx.x == 0) *out.done = 0;  // for the next launch
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int last = a.T - tile * tile_rows < tile_rows ? a.T : (tile + 1) * tile_rows;
     for (int pos = tile * tile_rows; pos < last;) {
@@ -459,25 +462,29 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
   if ((threadIdx.x & (kWave - 1)) == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
   double sum = 0.0;
-  for (int w = 0; w < (int)blockDim.x / kWave; ++w) sum += lds[w];
+  for (int w = 0; w < kThreads / kWave; ++w) sum += lds[w];
   return sum;
 }
 
-__device__ __forceinline__ void write_losses(const RouterArgs &a, double balance, double z, double full, double n) {
-  a.seq_tokens[a.S] = (int)full, a.seq_tokens[a.S + 1] = (int)n;
-  if (a.balance != nullptr) *a.balance = full > 0 ? (float)(balance / full) : 0.f;
-  if (a.z != nullptr) *a.z = n > 0 ? (float)(z / n) : 0.f;
-}
+// Visible to workgroups of other XCDs, whose L2 is another.
+__device__ __forceinline__ void publish(double *p, double v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ void publish(int *p, int v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <class T>
+__device__ __forceinline__ T published(const T *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// A sequence's slots: its counts, tokens and terms of the losses; with `parts` workgroups a sequence, each
-// for some of the columns. A workgroup of `lanes` x (threads / lanes): columns by slots.
-__global__ __launch_bounds__(kMaxThreads) void ep_router_sequences(const RouterArgs a, int tile_rows, Slots in, int parts,
-                                                                   int lanes) {
-  __shared__ double lds[kMaxThreads / kWave];
-  __shared__ double sums[kMaxThreads];
-  __shared__ int hits[kMaxThreads];
-  const int rows = blockDim.x / lanes, r = threadIdx.x / lanes, i = threadIdx.x % lanes;
-  for (int u = blockIdx.x; u < a.S * parts; u += gridDim.x) {
+// The slots of a sequence: its counts and tokens, and terms of the losses, `parts` workgroups a sequence with
+// LANES columns at a time each. The last workgroup to leave its terms adds them all, in order. The workgroup's
+// threads are LANES columns by slots.
+template <int LANES>
+__global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs a, int tile_rows, Slots in, int parts) {
+  __shared__ double lds[kThreads / kWave];
+  __shared__ double sums[kThreads];
+  __shared__ int hits[kThreads];
+  __shared__ bool last;
+  constexpr int kRows = kThreads / LANES;
+  const int r = threadIdx.x / LANES, i = threadIdx.x % LANES, units = a.S * parts;
+  int mine = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x, ++mine) {
     const int s = u / parts, part = u % parts;
     int b = 0, e = a.T;
     if (a.seq != nullptr) {
@@ -485,54 +492,61 @@ __global__ __launch_bounds__(kMaxThreads) void ep_router_sequences(const RouterA
       e = a.seq[s + 1] < a.T ? a.seq[s + 1] : a.T;
     }
     const int first = b < e ? b / tile_rows : 0, end = b < e ? (e - 1) / tile_rows + 1 : 0;
-    double tokens = 0.0, z = 0.0, sum = 0.0;
-    for (int t = first + threadIdx.x; t < end; t += blockDim.x) tokens += in.tokens[t + s], z += in.z[t + s];
-    const int c0 = part * lanes, step = parts * lanes;
-    for (int c = c0; c < a.E; c += step) {
+    int n = 0;
+    for (int t = first + threadIdx.x; t < end; t += kThreads) n += in.tokens[t + s];
+    double sum = 0.0;
+    for (int c = part * LANES + i; c - i < a.E; c += parts * LANES) {
       double p = 0.0;
       int hit = 0;
-      if (c + i < a.E) {
-#pragma unroll 4
-        for (int t = first + r; t < end; t += rows) {
-          const int64_t at = (int64_t)(t + s) * a.E + c + i;
+      if (c < a.E) {
+#pragma unroll 8
+        for (int t = first + r; t < end; t += kRows) {
+          const int64_t at = (int64_t)(t + s) * a.E + c;
           p += in.p[at], hit += in.counts[at];
         }
       }
       __syncthreads();
       sums[threadIdx.x] = p, hits[threadIdx.x] = hit;
       __syncthreads();
-      if (r == 0 && c + i < a.E) {
-        for (int k = 1; k < rows; ++k) p += sums[k * lanes + i], hit += hits[k * lanes + i];
-        a.counts[(int64_t)s * a.E + c + i] = hit;
+      if (r == 0 && c < a.E) {
+#pragma unroll
+        for (int k = 1; k < kRows; ++k) p += sums[k * LANES + i], hit += hits[k * LANES + i];
+        a.counts[(int64_t)s * a.E + c] = hit;
         sum += hit * p;
       }
     }
+    const double tokens = block_sum((double)n, lds);
     sum = block_sum(sum, lds);
-    tokens = block_sum(tokens, lds);
-    z = block_sum(z, lds);
-    if (threadIdx.x == 0) {
-      const double n = tokens;
-      if (part == 0) a.seq_tokens[s] = (int)n;
-      sum = n > 0 ? sum * a.E / ((double)a.K * n * n) : 0.0;
-      if (a.S * parts == 1) {
-        write_losses(a, sum, z, n > 0, n);
-      } else {
-        in.seq_balance[u] = sum;
-        in.seq_z[u] = part == 0 ? z : 0.0;
+    if (part == 0) {
+      double z = 0.0;
+      if (a.z != nullptr) {
+        for (int t = first + threadIdx.x; t < end; t += kThreads) z += in.z[t + s];
+        z = block_sum(z, lds);
       }
+      if (threadIdx.x == 0) publish(&in.seq_z[s], z), publish(&a.seq_tokens[s], (int)tokens);
     }
+    if (threadIdx.x == 0) publish(&in.balance[u], tokens > 0 ? sum * a.E / ((double)a.K * tokens * tokens) : 0.0);
   }
-}
-
-// The losses from the sequences' terms.
-__global__ __launch_bounds__(kThreads) void ep_router_losses(const RouterArgs a, Slots in, int parts) {
-  __shared__ double lds[kMaxThreads / kWave];
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(in.done, (unsigned)mine) + (unsigned)mine == (unsigned)units;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
   double balance = 0.0, z = 0.0, full = 0.0, n = 0.0;
-  for (int s = threadIdx.x; s < a.S * parts; s += kThreads) balance += in.seq_balance[s], z += in.seq_z[s];
-  for (int s = threadIdx.x; s < a.S; s += kThreads) n += a.seq_tokens[s], full += a.seq_tokens[s] > 0;
-  balance = block_sum(balance, lds), z = block_sum(z, lds);
-  n = block_sum(n, lds), full = block_sum(full, lds);
-  if (threadIdx.x == 0) write_losses(a, balance, z, full, n);
+  for (int u = threadIdx.x; u < units; u += kThreads) balance += published(&in.balance[u]);
+  for (int s = threadIdx.x; s < a.S; s += kThreads) {
+    const int tokens = published(&a.seq_tokens[s]);
+    z += published(&in.seq_z[s]), n += tokens, full += tokens > 0;
+  }
+  balance = block_sum(balance, lds), full = block_sum(full, lds), n = block_sum(n, lds);
+  if (a.z != nullptr) z = block_sum(z, lds);
+  if (threadIdx.x == 0) {
+    a.seq_tokens[a.S] = (int)full, a.seq_tokens[a.S + 1] = (int)n;
+    if (a.balance != nullptr) *a.balance = full > 0 ? (float)(balance / full) : 0.f;
+    if (a.z != nullptr) *a.z = n > 0 ? (float)(z / n) : 0.f;
+  }
 }
 
 template <bool FP32, int L, int V>
@@ -671,19 +685,31 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
   }
 }
 
-// Tokens per tile and slot: 64, one or four per group of lanes of a workgroup; 256 where those make too many slots.
-int tile_rows_of(int T) { return T > 64 * 1024 ? 256 : 64; }
-
-// Workgroups for the slots of a sequence: several where there are too many for one.
-constexpr int kMaxParts = 16;
-int parts_of(const RouterArgs &a, int64_t tiles) {
-  if (a.S > 1 || tiles <= 64) return 1;
-  return kMaxParts;
+// Tokens per tile, and so per slot: 16 as long as that leaves about a thousand tiles, at most 256.
+int tile_rows_of(int T) {
+  int rows = 16;
+  while (rows < 256 && T / rows > 1024) rows *= 2;
+  return rows;
 }
 
-int64_t slots_of(int T, int S) {
-  const int rows = tile_rows_of(T);
-  return (int64_t)(T + rows - 1) / rows + S;
+// Columns per workgroup of the second launch: the fewer, the more slots a sequence has.
+int lanes_of(int64_t tiles, int S) {
+  const int64_t slots = tiles / S;
+  return slots >= 256 ? 4 : (slots >= 64 ? 16 : 64);
+}
+
+struct Sizes {
+  int tile_rows, tiles, lanes, parts;
+  int64_t slots;
+};
+Sizes sizes_of(int T, int E, int S) {
+  Sizes z;
+  z.tile_rows = tile_rows_of(T);
+  z.tiles = (int)(((int64_t)T + z.tile_rows - 1) / z.tile_rows);
+  z.slots = (int64_t)z.tiles + S;
+  z.lanes = lanes_of(z.tiles, S);
+  z.parts = (E + z.lanes - 1) / z.lanes;
+  return z;
 }
 
 int64_t up(int64_t n) { return (n + 15) & ~(int64_t)15; }
@@ -703,47 +729,46 @@ int for_shape(int E, F f) {
 }  // namespace
 
 size_t router_workspace(int T, int E, int S) {
-  const int64_t slots = slots_of(T, S);
-  return (size_t)(2 * up(slots * E * 4) + 2 * up(slots * 4) + 2 * up((int64_t)(S + kMaxParts) * 8));
+  const Sizes z = sizes_of(T, E, S);
+  return (size_t)(2 * up(z.slots * E * 4) + 2 * up(z.slots * 4) + up((int64_t)S * z.parts * 8) + up((int64_t)S * 8) + up(4));
 }
 
 int launch_router(const RouterArgs &a) {
   const int cap = stream_workgroup_limit(a.stream);
-  const int rows = tile_rows_of(a.T), tiles = (a.T + rows - 1) / rows;
+  const Sizes z = sizes_of(a.T, a.E, a.S);
   Slots w{};
   if (a.counts != nullptr) {
-    const int64_t slots = slots_of(a.T, a.S);
     char *at = (char *)a.workspace;
     const auto take = [&](int64_t bytes) {
       char *p = at;
       at += up(bytes);
       return p;
     };
-    w.seq_balance = (double *)take((int64_t)(a.S + kMaxParts) * 8), w.seq_z = (double *)take((int64_t)(a.S + kMaxParts) * 8);
-    w.p = (float *)take(slots * a.E * 4), w.counts = (int *)take(slots * a.E * 4);
-    w.z = (float *)take(slots * 4), w.tokens = (int *)take(slots * 4);
+    w.balance = (double *)take((int64_t)a.S * z.parts * 8), w.seq_z = (double *)take((int64_t)a.S * 8);
+    w.p = (float *)take(z.slots * a.E * 4), w.counts = (int *)take(z.slots * a.E * 4);
+    w.z = (float *)take(z.slots * 4), w.tokens = (int *)take(z.slots * 4);
+    w.done = (unsigned *)take(4);
   }
-  if (a.T > 0) {
+  if (a.T > 0 || a.counts != nullptr) {
     const int rc = for_shape(a.E, [&](auto l, auto v) {
       constexpr int L = decltype(l)::value, V = decltype(v)::value;
-      // With statistics a tile's workgroup is large, so that few slots are left; without, small.
-      const int threads = a.counts != nullptr ? (cap > 0 ? kThreads : kMaxThreads) : 64;
-      const int per = a.counts != nullptr ? rows : threads / L;
-      const int n = (a.T + per - 1) / per, most = cap > 0 ? cap : 1 << 20;
-      const unsigned grid = (unsigned)(n < most ? n : most);
-      if (a.fp32) ep_router_rows<true, L, V><<<grid, threads, 0, a.stream>>>(a, per, n, w);
-      else ep_router_rows<false, L, V><<<grid, threads, 0, a.stream>>>(a, per, n, w);
+      // Without statistics a wave on its own is enough: more workgroups for a few tokens.
+      const int threads = a.counts != nullptr || cap > 0 ? kThreads : kWave;
+      const int rows = a.counts != nullptr ? z.tile_rows : threads / L;
+      const int n = (int)(((int64_t)a.T + rows - 1) / rows), most = cap > 0 ? cap : 1 << 20;
+      const unsigned grid = (unsigned)(n < most ? (n > 0 ? n : 1) : most);
+      if (a.fp32) ep_router_rows<true, L, V><<<grid, threads, 0, a.stream>>>(a, rows, n, w);
+      else ep_router_rows<false, L, V><<<grid, threads, 0, a.stream>>>(a, rows, n, w);
       return launch_status();
     });
     if (rc != 0) return rc;
   }
   if (a.counts == nullptr) return 0;
-  const int parts = parts_of(a, tiles);
-  const int lanes = parts > 1 ? 64 : (a.E <= 64 ? 64 : (a.E <= 128 ? 128 : 256)), units = a.S * parts;
-  ep_router_sequences<<<(unsigned)(cap > 0 && cap < units ? cap : units), kMaxThreads, 0, a.stream>>>(a, rows, w, parts, lanes);
-  if (const int rc = launch_status()) return rc;
-  if (units == 1) return 0;
-  ep_router_losses<<<1, kThreads, 0, a.stream>>>(a, w, parts);
+  const int64_t units = (int64_t)a.S * z.parts, most = cap > 0 ? cap : 1 << 20;
+  const unsigned grid = (unsigned)(units < most ? units : most);
+  if (z.lanes == 4) ep_router_sequences<4><<<grid, kThreads, 0, a.stream>>>(a, z.tile_rows, w, z.parts);
+  else if (z.lanes == 16) ep_router_sequences<16><<<grid, kThreads, 0, a.stream>>>(a, z.tile_rows, w, z.parts);
+  else ep_router_sequences<64><<<grid, kThreads, 0, a.stream>>>(a, z.tile_rows, w, z.parts);
   return launch_status();
 }
 
