@@ -19,6 +19,7 @@ namespace ep {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));  // a load takes any multiple of 4
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
@@ -89,7 +90,7 @@ __device__ __forceinline__ void load_row(const void *x, int64_t row, int E, int 
       const int c = column<L, V>(i, j);
       if (c >= E) continue;
       if constexpr (FP32) {
-        const f32x4 a = *(const f32x4 *)((const float *)x + row * E + c);
+        const f32x4_any a = *(const f32x4_any *)((const float *)x + row * E + c);
         v[j] = a[0];
         if constexpr (V >= 4) v[j + 1] = a[1], v[j + 2] = a[2], v[j + 3] = a[3];
       } else {
@@ -129,6 +130,28 @@ __device__ __forceinline__ float reference(bool sigmoid, float top) {
   return sigmoid ? fminf(top, 0.f) : top;
 }
 
+// Terms of a row, and their sum in the calling lane. Sigmoids need a second exponential only in rows
+// whose logits are all negative.
+template <int V>
+__device__ __forceinline__ float terms(bool sigmoid, const float (&v)[V], float ref, float (&e)[V]) {
+  float total = 0.f;
+  if (!sigmoid) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = __expf(v[j] - ref), total += e[j];
+  } else if (ballot(ref < 0.f) == 0) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float small = __expf(-fabsf(v[j])), by = __builtin_amdgcn_rcpf(1.0f + small);
+      e[j] = v[j] >= 0.f ? by : small * by;
+      total += e[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = term(true, v[j], ref), total += e[j];
+  }
+  return total;
+}
+
 // The sequence s with seq[s] <= t < seq[s + 1]: -1 before the first, S behind the last.
 __device__ __forceinline__ int sequence_of(const int32_t *seq, int S, int t) {
   if (seq == nullptr) return 0;
@@ -166,10 +189,10 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // instruction and names its column; x - m, as an unsigned number, puts what is still below the last
 // maximum m on top. bf16 logits fit whole. Of binary32 keys the lower bits are lost: then K + 2
 // candidates are taken and ranked by their whole keys, and the choice stands if what was
-// left out lies below the K-th whatever its lower bits are, and, for score + bias, if neighbours differ
-// by more than the keys' own rounding errors.
-// Exact: binary64 keys, one maximum at a time; for the rows where the fast way cannot tell, and for more
-// candidates than lanes.
+// left out lies below the K-th whatever its lower bits are. Candidates' scores + bias that differ by no more
+// than their rounding errors (one row in a thousand) are ranked again in binary64.
+// Exact: binary64 keys, one maximum at a time; for rows where what is left out may reach the K-th (many
+// equal keys), and for more candidates than lanes.
 template <int L, int V>
 struct Chooser {
   static constexpr int kColumnBits = (L * V <= 16 ? 4 : L * V <= 32 ? 5 : L * V <= 64 ? 6 : L * V <= 128 ? 7 : L * V <= 256 ? 8 : L * V <= 512 ? 9 : 10);
@@ -185,13 +208,20 @@ struct Chooser {
   static __device__ __forceinline__ uint32_t largest(const uint32_t (&x)[V], int C, int i) {
     uint32_t last = 0x80000000u, mine = 0;
     for (int k = 0; k < C; ++k) {
-      uint32_t best = x[0] - last;
+      uint32_t t[V];
 #pragma unroll
-      for (int j = 1; j < V; ++j) {
-        const uint32_t t = x[j] - last;
-        best = t > best ? t : best;
+      for (int j = 0; j < V; ++j) t[j] = x[j] - last;
+#pragma unroll
+      for (int n = V; n > 1; n = (n + 2) / 3) {  // maxima of three
+#pragma unroll
+        for (int j = 0; j < (n + 2) / 3; ++j) {
+          uint32_t m = t[3 * j];
+          if (3 * j + 1 < n) m = t[3 * j + 1] > m ? t[3 * j + 1] : m;
+          if (3 * j + 2 < n) m = t[3 * j + 2] > m ? t[3 * j + 2] : m;
+          t[j] = m;
+        }
       }
-      best = lanes_max<L>(best) + last;
+      const uint32_t best = lanes_max<L>(t[0]) + last;
       if (k == i) mine = best;
       last = best > 1 ? best : 1;
     }
@@ -203,35 +233,81 @@ struct Chooser {
     return unordered(packed >> kColumnBits << kLost | ((1u << kLost) - 1));
   }
 
-  // Rank of this lane's (key, column) among the row's lanes, and whether another key is within `near`.
-  static __device__ __forceinline__ int rank(float key, int column, int C, float near, bool &close) {
-    int r = 0;
-    const auto against = [&](float k, int c) {
-      r += k > key || (k == key && c < column);
-      close |= fabsf(k - key) <= near && c != column;
+  // f(key, column) of the row's other candidates.
+  template <class T, class F>
+  static __device__ __forceinline__ void others(T key, int column, int C, F f) {
+    const auto rotated = [](T k, auto n) {
+      if constexpr (sizeof(T) == 4) {
+        return __int_as_float(rotate<decltype(n)::value>(__float_as_int(k)));
+      } else {
+        const uint64_t v = __builtin_bit_cast(uint64_t, k);
+        const uint32_t lo = (uint32_t)rotate<decltype(n)::value>((int)(uint32_t)v), hi = (uint32_t)rotate<decltype(n)::value>((int)(v >> 32));
+        return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+      }
     };
     if constexpr (L == 16) {
-#define EP_AGAINST(N) against(__int_as_float(rotate<N>(__float_as_int(key))), rotate<N>(column));
-      EP_AGAINST(1) EP_AGAINST(2) EP_AGAINST(3) EP_AGAINST(4) EP_AGAINST(5) EP_AGAINST(6) EP_AGAINST(7) EP_AGAINST(8)
-      EP_AGAINST(9) EP_AGAINST(10) EP_AGAINST(11) EP_AGAINST(12) EP_AGAINST(13) EP_AGAINST(14) EP_AGAINST(15)
-#undef EP_AGAINST
+#define EP_OTHER(N) f(rotated(key, std::integral_constant<int, N>()), rotate<N>(column));
+      EP_OTHER(1) EP_OTHER(2) EP_OTHER(3) EP_OTHER(4) EP_OTHER(5) EP_OTHER(6) EP_OTHER(7) EP_OTHER(8)
+      EP_OTHER(9) EP_OTHER(10) EP_OTHER(11) EP_OTHER(12) EP_OTHER(13) EP_OTHER(14) EP_OTHER(15)
+#undef EP_OTHER
     } else {
-      for (int c = 0; c < C; ++c) against(read_lane(key, c), read_lane(column, c));
+      for (int c = 0; c < C; ++c) {
+        if constexpr (sizeof(T) == 4) {
+          f(read_lane(key, c), read_lane(column, c));
+        } else {
+          const uint64_t v = __builtin_bit_cast(uint64_t, key);
+          const uint32_t lo = (uint32_t)read_lane((int)(uint32_t)v, c), hi = (uint32_t)read_lane((int)(v >> 32), c);
+          f(__builtin_bit_cast(T, (uint64_t)hi << 32 | lo), read_lane(column, c));
+        }
+      }
     }
+  }
+  // Rank of this lane's (key, column) among the row's lanes, and whether another key is within `near`.
+  template <class T>
+  static __device__ __forceinline__ int rank(T key, int column, int C, float near, bool &close) {
+    int r = 0;
+    others(key, column, C, [&](T k, int c) {
+      r += k > key || (k == key && c < column);
+      if constexpr (sizeof(T) == 4) close |= fabsf(k - key) <= near && c != column;
+    });
     return r;
   }
 
-  // Exact: ids[b] of lane i is place b * L + i (-1: none left).
-  static __device__ __forceinline__ void exactly(double (&key)[V], int i, int K, int (&ids)[64 / L]) {
+  // Exact: ids[b] of lane i is place b * L + i (-1: none left). Rare, so it reads the row again for every
+  // maximum instead of keeping binary64 keys in registers.
+  template <bool FP32>
+  static __device__ __forceinline__ void exactly(const RouterArgs &a, int64_t row, bool on, float ref, int i, int (&ids)[64 / L]) {
+    double sum = 1.0;
+    if (a.bias != nullptr && !a.sigmoid) {
+      sum = 0.0;
+#pragma unroll 1
+      for (int j = 0; j < V; ++j) {
+        const int c = column<L, V>(i, j);
+        if (on && c < a.E) sum += exp((double)load_one<FP32>(a.logits, row * a.E + c) - (double)ref);
+      }
+#pragma unroll
+      for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
+    }
+    double last = (double)kInf;
+    int last_at = -1;
 #pragma unroll
     for (int b = 0; b < 64 / L; ++b) {
       ids[b] = -1;
-      for (int k = b * L; k < K && k < (b + 1) * L; ++k) {
+      for (int k = b * L; k < a.K && k < (b + 1) * L; ++k) {
         double best = -(double)kInf;
         int at = 1 << 30;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (key[j] > best) best = key[j], at = column<L, V>(i, j);
+#pragma unroll 1
+        for (int j = 0; j < V; ++j) {
+          const int c = column<L, V>(i, j);
+          if (!on || c >= a.E) continue;
+          const float l = load_one<FP32>(a.logits, row * a.E + c);
+          if (!(l > -kInf)) continue;
+          double key = l;
+          if (a.bias != nullptr)
+            key = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)ref) / sum) + (double)a.bias[c];
+          // what comes behind the last one, and before the best so far
+          if ((key < last || (key == last && c > last_at)) && key > best) best = key, at = c;
+        }
 #pragma unroll
         for (int d = 1; d < L; d *= 2) {
           const double other = __shfl_xor(best, d);
@@ -239,32 +315,27 @@ struct Chooser {
           if (other > best || (other == best && o < at)) best = other, at = o;
         }
         if (k % L == i && best > -(double)kInf) ids[b] = at;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (column<L, V>(i, j) == at) key[j] = -(double)kInf;
+        last = best, last_at = at;
       }
     }
   }
 };
 
-template <bool FP32, int L, int V>
-__global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
+template <bool FP32, bool STATS, int L, int V>
+__global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
   constexpr int KB = 64 / L, kWaveRows = kWave / L, kWaves = kThreads / kWave;
-  __shared__ float sums[kWaves][L * V];
-  __shared__ int hits[L * V];
-  __shared__ float zs[kWaves * kWaveRows];
-  __shared__ int taken[kWaves * kWaveRows];
+  __shared__ float sums[STATS ? kWaves : 1][STATS ? L * V : 1];
+  __shared__ int hits[STATS ? L * V : 1];
+  __shared__ float zs[STATS ? kWaves * kWaveRows : 1];
+  __shared__ int taken[STATS ? kWaves * kWaveRows : 1];
   const int i = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L, E = a.E, K = a.K;
-  const bool stats = a.counts != nullptr;
+  constexpr bool stats = STATS;
   const bool packed_whole = !FP32 && a.bias == nullptr;  // no key bits are lost
   const int candidates = packed_whole ? K : (K + 2 < E ? K + 2 : E);
   const bool fast = candidates <= L;
   const bool all_terms = stats || a.bias != nullptr || !(a.normalize || a.sigmoid);
-  float bias[V];  // of this lane's columns
-#pragma unroll
-  for (int j = 0; j < V; ++j) bias[j] = a.bias != nullptr && column<L, V>(i, j) < E ? a.bias[column<L, V>(i, j)] : 0.f;
   if (stats && blockIdx.x == 0 && threadIdx.x == 0) *out.done = 0;  // for the next launch
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int last = a.T - tile * tile_rows < tile_rows ? a.T : (tile + 1) * tile_rows;
@@ -274,12 +345,12 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
         s = sequence_of(a.seq, a.S, pos);
         if (s < a.S) end = a.seq[s + 1] < last ? a.seq[s + 1] : last;
       }
-      const bool inside = stats && s >= 0 && s < a.S;
+      const bool inside = STATS && s >= 0 && s < a.S;
       float acc[V], z = 0.f;
       int count = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = 0.f;
-      if (inside) {
+      if (STATS && inside) {
         for (int c = threadIdx.x; c < E; c += blockDim.x) hits[c] = 0;
         __syncthreads();
       }
@@ -295,24 +366,25 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
           for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
           top = lanes_max<L>(top);
           ref = reference(a.sigmoid, top);
-#pragma unroll
-          for (int j = 0; j < V; ++j) e[j] = term(a.sigmoid, v[j], ref), total += e[j];
-          total = lanes_sum<L>(total);
+          total = lanes_sum<L>(terms(a.sigmoid, v, ref, e));
         }
         int ids[KB], places[KB];  // of this lane
 #pragma unroll
         for (int b = 0; b < KB; ++b) places[b] = b * L + i, ids[b] = -1;
         if (!a.given) {
           const float back = a.sigmoid ? (ref < 0.f ? __expf(ref) : 1.0f) : (total == 0.f ? 0.f : 1.0f / total);
-          const auto key_of = [&](int j) {
-            if (a.bias == nullptr) return v[j];
-            return v[j] > -kInf ? e[j] * back + bias[j] : -kInf;
-          };
           bool unsure = !fast;
           if (fast) {
             uint32_t x[V];
+            if (a.bias == nullptr) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = Choice::pack(key_of(j), column<L, V>(i, j));
+              for (int j = 0; j < V; ++j) x[j] = Choice::pack(v[j], column<L, V>(i, j));
+            } else {
+              float bias[V];
+              load_row<true, L, V>(a.bias, 0, E, i, true, bias);
+#pragma unroll
+              for (int j = 0; j < V; ++j) x[j] = Choice::pack(v[j] > -kInf ? e[j] * back + bias[j] : -kInf, column<L, V>(i, j));
+            }
             const uint32_t mine = Choice::largest(x, candidates, i);
             const bool valid = mine != 0 && i < candidates;
             ids[0] = valid ? Choice::column_of(mine) : -1;
@@ -332,31 +404,30 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
               // what was left out lies below the last candidate's packed number
               const uint32_t left = (uint32_t)__shfl((int)mine, (int)(threadIdx.x & (kWave - 1)) / L * L + candidates - 1);
               const bool rest = candidates < E && left != 0;
-              unsure = valid && ((close && places[0] <= K) || (rest && places[0] == K - 1 && !(key > Choice::at_most(left) + fmaxf(near, 0.f))));
+              unsure = valid && rest && places[0] == K - 1 && !(key > Choice::at_most(left) + fmaxf(near, 0.f));
+              if (ballot(close && valid && places[0] <= K) != 0) {  // only with a bias: the candidates again, in binary64
+                double sum = 1.0;
+                if (!a.sigmoid) {
+                  sum = 0.0;
+#pragma unroll
+                  for (int j = 0; j < V; ++j) sum += exp((double)v[j] - (double)ref);
+#pragma unroll
+                  for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
+                }
+                double exact = -(double)kInf;
+                if (valid) {
+                  const double l = load_one<FP32>(a.logits, (int64_t)row * E + ids[0]);
+                  exact = (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)ref) / sum) + (double)a.bias[ids[0]];
+                }
+                places[0] = Choice::rank(exact, valid ? ids[0] : E + i, candidates, near, close);
+              }
               if (places[0] >= K) ids[0] = -1;
             }
           }
           unsure = lanes_any<L>(unsure && there);
           if (ballot(unsure) != 0) {
-            double key[V];
-            double sum = 0.0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              key[j] = v[j];
-              if (a.bias != nullptr) {
-                key[j] = a.sigmoid ? 1.0 / (1.0 + exp(-(double)v[j])) : exp((double)v[j] - (double)ref);
-                sum += key[j];
-              }
-            }
-            if (a.bias != nullptr) {
-#pragma unroll
-              for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
-#pragma unroll
-              for (int j = 0; j < V; ++j)
-                key[j] = v[j] > -kInf ? (a.sigmoid ? key[j] : key[j] / sum) + (double)bias[j] : -(double)kInf;
-            }
             int exact[KB];
-            Choice::exactly(key, i, K, exact);
+            Choice::template exactly<FP32>(a, row, on, ref, i, exact);
             if (unsure) {
 #pragma unroll
               for (int b = 0; b < KB; ++b) ids[b] = exact[b], places[b] = b * L + i;
@@ -407,7 +478,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
             if (a.weights != nullptr) a.weights[at] = w[b];
           }
         }
-        if (inside && any) {
+        if (STATS && inside && any) {
           const float by = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
           for (int j = 0; j < V; ++j) acc[j] += e[j] * by;
@@ -419,7 +490,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_rows(const RouterArgs a, i
             if (ids[b] >= 0) atomicAdd(&hits[ids[b]], 1);
         }
       }
-      if (inside) {
+      if (STATS && inside) {
         // a wave's rows first, then the waves in order
         const int wave = threadIdx.x / kWave;
 #pragma unroll
@@ -492,8 +563,6 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
       e = a.seq[s + 1] < a.T ? a.seq[s + 1] : a.T;
     }
     const int first = b < e ? b / tile_rows : 0, end = b < e ? (e - 1) / tile_rows + 1 : 0;
-    int n = 0;
-    for (int t = first + threadIdx.x; t < end; t += kThreads) n += in.tokens[t + s];
     double sum = 0.0;
     for (int c = part * LANES + i; c - i < a.E; c += parts * LANES) {
       double p = 0.0;
@@ -515,17 +584,15 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
         sum += hit * p;
       }
     }
-    const double tokens = block_sum((double)n, lds);
     sum = block_sum(sum, lds);
+    if (threadIdx.x == 0) publish(&in.balance[u], sum);
     if (part == 0) {
-      double z = 0.0;
-      if (a.z != nullptr) {
-        for (int t = first + threadIdx.x; t < end; t += kThreads) z += in.z[t + s];
-        z = block_sum(z, lds);
-      }
-      if (threadIdx.x == 0) publish(&in.seq_z[s], z), publish(&a.seq_tokens[s], (int)tokens);
+      double n = 0.0, z = 0.0;
+      for (int t = first + threadIdx.x; t < end; t += kThreads) n += in.tokens[t + s], z += in.z[t + s];
+      n = block_sum(n, lds);
+      if (a.z != nullptr) z = block_sum(z, lds);
+      if (threadIdx.x == 0) publish(&in.seq_z[s], z), publish(&a.seq_tokens[s], (int)n);
     }
-    if (threadIdx.x == 0) publish(&in.balance[u], tokens > 0 ? sum * a.E / ((double)a.K * tokens * tokens) : 0.0);
   }
   if (threadIdx.x == 0) {
     __threadfence();
@@ -535,7 +602,10 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
   __syncthreads();
   if (!last) return;
   double balance = 0.0, z = 0.0, full = 0.0, n = 0.0;
-  for (int u = threadIdx.x; u < units; u += kThreads) balance += published(&in.balance[u]);
+  for (int u = threadIdx.x; u < units; u += kThreads) {
+    const double tokens = published(&a.seq_tokens[u / parts]);
+    if (tokens > 0) balance += published(&in.balance[u]) * a.E / (a.K * tokens * tokens);
+  }
   for (int s = threadIdx.x; s < a.S; s += kThreads) {
     const int tokens = published(&a.seq_tokens[s]);
     z += published(&in.seq_z[s]), n += tokens, full += tokens > 0;
@@ -583,9 +653,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
     top = lanes_max<L>(top);
     const float ref = reference(a.sigmoid, top);
     float p[V], total = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = term(a.sigmoid, v[j], ref), total += p[j];
-    total = lanes_sum<L>(total);
+    total = lanes_sum<L>(terms(a.sigmoid, v, ref, p));
     const float by = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] *= by;
@@ -757,9 +825,12 @@ int launch_router(const RouterArgs &a) {
       const int rows = a.counts != nullptr ? z.tile_rows : threads / L;
       const int n = (int)(((int64_t)a.T + rows - 1) / rows), most = cap > 0 ? cap : 1 << 20;
       const unsigned grid = (unsigned)(n < most ? (n > 0 ? n : 1) : most);
-      if (a.fp32) ep_router_rows<true, L, V><<<grid, threads, 0, a.stream>>>(a, rows, n, w);
-      else ep_router_rows<false, L, V><<<grid, threads, 0, a.stream>>>(a, rows, n, w);
-      return launch_status();
+      const auto run = [&](auto kernel) {
+        kernel<<<grid, threads, 0, a.stream>>>(a, rows, n, w);
+        return launch_status();
+      };
+      if (a.counts != nullptr) return a.fp32 ? run(ep_router_rows<true, true, L, V>) : run(ep_router_rows<false, true, L, V>);
+      return a.fp32 ? run(ep_router_rows<true, false, L, V>) : run(ep_router_rows<false, false, L, V>);
     });
     if (rc != 0) return rc;
   }

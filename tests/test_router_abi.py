@@ -75,8 +75,9 @@ def test_router_workspace():
     assert size(4, 16, (1 << 16) + 1) == 0
     assert 0 < size(0, 16, 1) <= 1024
     for T, E, S in [(1, 1, 1), (4096, 256, 1), (4096, 256, 300), (100000, 1024, 7)]:
-        # a sum and a count per expert for every tile of tokens and every sequence, at most one tile in 16 tokens
-        assert size(T, E, S) <= (T // 16 + 1 + S) * (8 * E + 8) + 16 * S + 128
+        # a sum and a count per expert for every tile of tokens and every sequence, at most one tile in 16 tokens;
+        # for every sequence its terms of the losses, at most one for four experts
+        assert size(T, E, S) <= (T // 16 + 1 + S) * (8 * E + 8) + S * (8 * (E // 4 + 1) + 8) + 128
         assert size(2 * T, E, S) >= size(T, E, S) and size(T, E, S + 1) >= size(T, E, S)
 
 
