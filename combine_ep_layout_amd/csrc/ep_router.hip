@@ -325,11 +325,11 @@ template <bool FP32, bool STATS, int L, int V>
 __global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
-  constexpr int KB = 64 / L, kWaveRows = kWave / L, kWaves = kThreads / kWave;
+  constexpr int KB = 64 / L, kWaves = kThreads / kWave;
   __shared__ float sums[STATS ? kWaves : 1][STATS ? L * V : 1];
   __shared__ int hits[STATS ? L * V : 1];
-  __shared__ float zs[STATS ? kWaves * kWaveRows : 1];
-  __shared__ int taken[STATS ? kWaves * kWaveRows : 1];
+  __shared__ float zs[kWaves];
+  __shared__ int taken[kWaves];
   const int i = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L, E = a.E, K = a.K;
   constexpr bool stats = STATS;
   const bool packed_whole = !FP32 && a.bias == nullptr;  // no key bits are lost
@@ -501,7 +501,11 @@ __global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a
           }
           if ((threadIdx.x & (kWave - 1)) < L) sums[wave][column<L, V>(i, j)] = acc[j];
         }
-        if (i == 0) zs[group] = z, taken[group] = count;
+        if constexpr (L == 16) {
+          z += __shfl_xor(z, 16), count += __shfl_xor(count, 16);
+          z += __shfl_xor(z, 32), count += __shfl_xor(count, 32);
+        }
+        if ((threadIdx.x & (kWave - 1)) == 0) zs[wave] = z, taken[wave] = count;
         __syncthreads();
         const int64_t slot = tile + s;
         const int waves = blockDim.x / kWave;
@@ -514,7 +518,7 @@ __global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a
         if (threadIdx.x == 0) {
           float sum = 0.f;
           int n = 0;
-          for (int g = 0; g < groups; ++g) sum += zs[g], n += taken[g];
+          for (int g = 0; g < waves; ++g) sum += zs[g], n += taken[g];
           out.z[slot] = sum;
           out.tokens[slot] = n;
         }
@@ -525,16 +529,24 @@ __global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a
   }
 }
 
-// Sum over a workgroup, in a fixed order.
-__device__ __forceinline__ double block_sum(double v, double *lds) {
+// Sums over a workgroup, in a fixed order.
+template <int N>
+__device__ __forceinline__ void block_sums(double (&v)[N], double (&lds)[N][kThreads / kWave]) {
 #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
+  for (int d = 1; d < kWave; d *= 2)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], d);
   __syncthreads();
-  if ((threadIdx.x & (kWave - 1)) == 0) lds[threadIdx.x / kWave] = v;
+  if ((threadIdx.x & (kWave - 1)) == 0)
+#pragma unroll
+    for (int n = 0; n < N; ++n) lds[n][threadIdx.x / kWave] = v[n];
   __syncthreads();
-  double sum = 0.0;
-  for (int w = 0; w < kThreads / kWave; ++w) sum += lds[w];
-  return sum;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] = lds[n][0];
+#pragma unroll
+    for (int w = 1; w < kThreads / kWave; ++w) v[n] += lds[n][w];
+  }
 }
 
 // Visible to workgroups of other XCDs, whose L2 is another.
@@ -548,12 +560,12 @@ __device__ __forceinline__ T published(const T *p) { return __hip_atomic_load(p,
 // threads are LANES columns by slots.
 template <int LANES>
 __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs a, int tile_rows, Slots in, int parts) {
-  __shared__ double lds[kThreads / kWave];
-  __shared__ double sums[kThreads];
-  __shared__ int hits[kThreads];
+  constexpr int kRows = kThreads / LANES, kWaves = kThreads / kWave;
+  __shared__ double lds[4][kWaves];
+  __shared__ double sums[kWaves][LANES];
+  __shared__ int hits[kWaves][LANES];
   __shared__ bool last;
-  constexpr int kRows = kThreads / LANES;
-  const int r = threadIdx.x / LANES, i = threadIdx.x % LANES, units = a.S * parts;
+  const int r = threadIdx.x / LANES, i = threadIdx.x % LANES, wave = threadIdx.x / kWave, units = a.S * parts;
   int mine = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x, ++mine) {
     const int s = u / parts, part = u % parts;
@@ -563,35 +575,35 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
       e = a.seq[s + 1] < a.T ? a.seq[s + 1] : a.T;
     }
     const int first = b < e ? b / tile_rows : 0, end = b < e ? (e - 1) / tile_rows + 1 : 0;
-    double sum = 0.0;
-    for (int c = part * LANES + i; c - i < a.E; c += parts * LANES) {
-      double p = 0.0;
-      int hit = 0;
-      if (c < a.E) {
+    const int c = part * LANES + i;
+    double p = 0.0, n = 0.0, z = 0.0;
+    int hit = 0;
+    if (c < a.E) {
 #pragma unroll 8
-        for (int t = first + r; t < end; t += kRows) {
-          const int64_t at = (int64_t)(t + s) * a.E + c;
-          p += in.p[at], hit += in.counts[at];
-        }
-      }
-      __syncthreads();
-      sums[threadIdx.x] = p, hits[threadIdx.x] = hit;
-      __syncthreads();
-      if (r == 0 && c < a.E) {
-#pragma unroll
-        for (int k = 1; k < kRows; ++k) p += sums[k * LANES + i], hit += hits[k * LANES + i];
-        a.counts[(int64_t)s * a.E + c] = hit;
-        sum += hit * p;
+      for (int t = first + r; t < end; t += kRows) {
+        const int64_t at = (int64_t)(t + s) * a.E + c;
+        p += in.p[at], hit += in.counts[at];
       }
     }
-    sum = block_sum(sum, lds);
-    if (threadIdx.x == 0) publish(&in.balance[u], sum);
-    if (part == 0) {
-      double n = 0.0, z = 0.0;
+    if (part == 0)
       for (int t = first + threadIdx.x; t < end; t += kThreads) n += in.tokens[t + s], z += in.z[t + s];
-      n = block_sum(n, lds);
-      if (a.z != nullptr) z = block_sum(z, lds);
-      if (threadIdx.x == 0) publish(&in.seq_z[s], z), publish(&a.seq_tokens[s], (int)n);
+#pragma unroll
+    for (int d = LANES; d < kWave; d *= 2) p += __shfl_xor(p, d), hit += __shfl_xor(hit, d);
+    __syncthreads();
+    if ((threadIdx.x & (kWave - 1)) < LANES) sums[wave][i] = p, hits[wave][i] = hit;
+    __syncthreads();
+    double sum = 0.0;
+    if (threadIdx.x < LANES && c < a.E) {
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) p += sums[w][i], hit += hits[w][i];
+      a.counts[(int64_t)s * a.E + c] = hit;
+      sum = hit * p;
+    }
+    double v[4] = {sum, n, z, 0.0};
+    block_sums(v, lds);
+    if (threadIdx.x == 0) {
+      publish(&in.balance[u], v[0]);
+      if (part == 0) publish(&in.seq_z[s], v[2]), publish(&a.seq_tokens[s], (int)v[1]);
     }
   }
   if (threadIdx.x == 0) {
@@ -601,22 +613,42 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
   }
   __syncthreads();
   if (!last) return;
-  double balance = 0.0, z = 0.0, full = 0.0, n = 0.0;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};  // balance, z, sequences with tokens, tokens
   for (int u = threadIdx.x; u < units; u += kThreads) {
     const double tokens = published(&a.seq_tokens[u / parts]);
-    if (tokens > 0) balance += published(&in.balance[u]) * a.E / (a.K * tokens * tokens);
+    const double term = published(&in.balance[u]);
+    if (tokens > 0) v[0] += term * a.E / (a.K * tokens * tokens);
   }
   for (int s = threadIdx.x; s < a.S; s += kThreads) {
     const int tokens = published(&a.seq_tokens[s]);
-    z += published(&in.seq_z[s]), n += tokens, full += tokens > 0;
+    v[1] += published(&in.seq_z[s]), v[2] += tokens > 0, v[3] += tokens;
   }
-  balance = block_sum(balance, lds), full = block_sum(full, lds), n = block_sum(n, lds);
-  if (a.z != nullptr) z = block_sum(z, lds);
+  block_sums(v, lds);
   if (threadIdx.x == 0) {
-    a.seq_tokens[a.S] = (int)full, a.seq_tokens[a.S + 1] = (int)n;
-    if (a.balance != nullptr) *a.balance = full > 0 ? (float)(balance / full) : 0.f;
-    if (a.z != nullptr) *a.z = n > 0 ? (float)(z / n) : 0.f;
+    a.seq_tokens[a.S] = (int)v[2], a.seq_tokens[a.S + 1] = (int)v[3];
+    if (a.balance != nullptr) *a.balance = v[2] > 0 ? (float)(v[0] / v[2]) : 0.f;
+    if (a.z != nullptr) *a.z = v[3] > 0 ? (float)(v[1] / v[3]) : 0.f;
   }
+}
+
+// sequence_of by all of a row's lanes: L of the remaining offsets at a time.
+template <int L>
+__device__ __forceinline__ int sequence_by_lanes(const int32_t *seq, int S, int t, int i) {
+  if (seq == nullptr) return 0;
+  int lo = 0, n = S + 1;  // the first lo offsets are at most t, those from lo + n on are not
+  while (ballot(n > 0) != 0) {
+    const int step = (n + L - 1) / L, at = lo + i * step;
+    const bool below = i * step < n && seq[i * step < n ? at : 0] <= t;
+    const int found = over_lanes<L>((int)below, [](int a, int b) { return a + b; });
+    const int left = n;
+    if (found == 0) {
+      n = 0;
+    } else {
+      const int skip = (found - 1) * step + 1;
+      lo += skip, n = left - skip < step - 1 ? left - skip : step - 1;
+    }
+  }
+  return lo - 1;
 }
 
 template <bool FP32, int L, int V>
@@ -633,7 +665,9 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
     const bool there = row < a.T;
     float v[V];
     load_row<FP32, L, V>(a.logits, row, E, i, there, v);
-    int ids[KB], any = 0;
+    const int s = a.counts != nullptr ? sequence_by_lanes<L>(a.seq, a.S, (int)(there ? row : 0), i) : -1;
+    int ids[KB];
+    bool any = false;
     float l[KB], dw[KB], most = -kInf;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -679,13 +713,38 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
       for (int b = 0; b < KB; ++b)
         d[b] = ids[b] < 0 ? 0.f : (a.sigmoid ? dw[b] * term(true, l[b], 0.f) * term(true, -l[b], 0.f) : dw[b]);
     }
-    // the entries of an id are added in order, so that an id that occurs twice gets one sum
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-      for (int k = 0; k < L && b * L + k < K; ++k) {
-        if (i == k && ids[b] >= 0) mine[ids[b]] += d[b];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // keeps the lanes' turns apart
+    // The entries of an id are added by the first of them, in a fixed order.
+    if (K <= L) {
+      float sum = 0.f;
+      bool mine_first = true;
+      if constexpr (L == 16) {
+        const auto with = [&](float v, int id, int lane) {
+          if (id != ids[0]) return;
+          sum += v;
+          mine_first &= lane >= i;
+        };
+        with(d[0], ids[0], i);
+#define EP_WITH(N) with(__int_as_float(rotate<N>(__float_as_int(d[0]))), rotate<N>(ids[0]), rotate<N>(i));
+        EP_WITH(1) EP_WITH(2) EP_WITH(3) EP_WITH(4) EP_WITH(5) EP_WITH(6) EP_WITH(7) EP_WITH(8)
+        EP_WITH(9) EP_WITH(10) EP_WITH(11) EP_WITH(12) EP_WITH(13) EP_WITH(14) EP_WITH(15)
+#undef EP_WITH
+      } else {
+        for (int k = 0; k < K; ++k) {
+          if (read_lane(ids[0], k) != ids[0]) continue;
+          sum += read_lane(d[0], k);
+          mine_first &= k >= i;
+        }
       }
+      if (ids[0] >= 0 && mine_first) mine[ids[0]] = sum;
+    } else {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+        for (int k = 0; k < L && b * L + k < K; ++k) {
+          if (i == k && ids[b] >= 0) mine[ids[b]] += d[b];
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // keeps the lanes' turns apart
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     float out[V], dot = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -702,7 +761,6 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
 #pragma unroll
       for (int j = 0; j < V; ++j) out[j] = p[j] * (out[j] - dot);
     }
-    const int s = a.counts != nullptr && there ? sequence_of(a.seq, a.S, (int)row) : -1;
     if (any && s >= 0 && s < a.S) {
       if (a.d_balance != nullptr) {
         const float n = (float)a.seq_tokens[s], full = (float)a.seq_tokens[a.S];
