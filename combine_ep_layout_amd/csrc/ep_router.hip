@@ -20,6 +20,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));  // a load takes any multiple of 4
+typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
@@ -322,7 +323,7 @@ struct Chooser {
 };
 
 template <bool FP32, bool STATS, int L, int V>
-__global__ __launch_bounds__(kThreads, 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
+__global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
   constexpr int KB = 64 / L, kWaves = kThreads / kWave;
@@ -651,9 +652,10 @@ __device__ __forceinline__ int sequence_by_lanes(const int32_t *seq, int S, int 
   return lo - 1;
 }
 
-template <bool FP32, int L, int V>
+// KB: places of a token's ids per lane.
+template <bool FP32, int L, int V, int KB>
 __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const RouterBackwardArgs a, int64_t steps) {
-  constexpr int KB = 64 / L, kGroups = kThreads / L;
+  constexpr int kGroups = kThreads / L;
   __shared__ float extra[kGroups][L * V];
   const int i = threadIdx.x % L, group = threadIdx.x / L, E = a.E, K = a.K;
   float *const mine = extra[group];
@@ -714,7 +716,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
         d[b] = ids[b] < 0 ? 0.f : (a.sigmoid ? dw[b] * term(true, l[b], 0.f) * term(true, -l[b], 0.f) : dw[b]);
     }
     // The entries of an id are added by the first of them, in a fixed order.
-    if (K <= L) {
+    if constexpr (KB == 1) {
       float sum = 0.f;
       bool mine_first = true;
       if constexpr (L == 16) {
@@ -766,12 +768,24 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
         const float n = (float)a.seq_tokens[s], full = (float)a.seq_tokens[a.S];
         const float f = n > 0.f && full > 0.f ? db * ((float)E / ((float)K * n * n * full)) : 0.f;
         float g[V], dot = 0.f;
+        if (V >= 4 && E % 4 == 0) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int c = column<L, V>(i, j);
-          g[j] = c < E ? f * (float)a.counts[(int64_t)s * E + c] : 0.f;
-          dot += p[j] * g[j];
+          for (int j = 0; j < V; j += 4) {
+            const int c = column<L, V>(i, j);
+            i32x4_any n = {0, 0, 0, 0};
+            if (c < E) n = *(const i32x4_any *)(a.counts + (int64_t)s * E + c);
+#pragma unroll
+            for (int k = 0; k < 4 && j + k < V; ++k) g[j + k] = f * (float)n[k];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const int c = column<L, V>(i, j);
+            g[j] = c < E ? f * (float)a.counts[(int64_t)s * E + c] : 0.f;
+          }
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) dot += p[j] * g[j];
         dot = lanes_sum<L>(dot);
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -909,9 +923,12 @@ int launch_router_backward(const RouterBackwardArgs &a) {
     const int64_t steps = ((int64_t)a.T + kThreads / L - 1) / (kThreads / L);
     const int64_t most = cap > 0 ? cap : 1 << 22;
     const unsigned grid = (unsigned)(steps < most ? steps : most);
-    if (a.fp32) ep_router_backward_rows<true, L, V><<<grid, kThreads, 0, a.stream>>>(a, steps);
-    else ep_router_backward_rows<false, L, V><<<grid, kThreads, 0, a.stream>>>(a, steps);
-    return launch_status();
+    const auto run = [&](auto kernel) {
+      kernel<<<grid, kThreads, 0, a.stream>>>(a, steps);
+      return launch_status();
+    };
+    if (a.K <= L) return a.fp32 ? run(ep_router_backward_rows<true, L, V, 1>) : run(ep_router_backward_rows<false, L, V, 1>);
+    return a.fp32 ? run(ep_router_backward_rows<true, L, V, 64 / L>) : run(ep_router_backward_rows<false, L, V, 64 / L>);
   });
 }
 
