@@ -276,8 +276,8 @@ struct Chooser {
 
   // Exact: ids[b] of lane i is place b * L + i (-1: none left). Rare, so it reads the row again for every
   // maximum instead of keeping binary64 keys in registers.
-  template <bool FP32>
-  static __device__ __forceinline__ void exactly(const RouterArgs &a, int64_t row, bool on, float ref, int i, int (&ids)[64 / L]) {
+  template <bool FP32, int KB>
+  static __device__ __forceinline__ void exactly(const RouterArgs &a, int64_t row, bool on, float ref, int i, int (&ids)[KB]) {
     double sum = 1.0;
     if (a.bias != nullptr && !a.sigmoid) {
       sum = 0.0;
@@ -292,7 +292,7 @@ struct Chooser {
     double last = (double)kInf;
     int last_at = -1;
 #pragma unroll
-    for (int b = 0; b < 64 / L; ++b) {
+    for (int b = 0; b < KB; ++b) {
       ids[b] = -1;
       for (int k = b * L; k < a.K && k < (b + 1) * L; ++k) {
         double best = -(double)kInf;
@@ -322,11 +322,11 @@ struct Chooser {
   }
 };
 
-template <bool FP32, bool STATS, int L, int V>
+template <bool FP32, bool STATS, int L, int V, int KB>
 __global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
-  constexpr int KB = 64 / L, kWaves = kThreads / kWave;
+  constexpr int kWaves = kThreads / kWave;
   __shared__ float sums[STATS ? kWaves : 1][STATS ? L * V : 1];
   __shared__ int hits[STATS ? L * V : 1];
   __shared__ float zs[kWaves];
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_
           unsure = lanes_any<L>(unsure && there);
           if (ballot(unsure) != 0) {
             int exact[KB];
-            Choice::template exactly<FP32>(a, row, on, ref, i, exact);
+            Choice::template exactly<FP32, KB>(a, row, on, ref, i, exact);
             if (unsure) {
 #pragma unroll
               for (int b = 0; b < KB; ++b) ids[b] = exact[b], places[b] = b * L + i;
@@ -901,8 +901,15 @@ int launch_router(const RouterArgs &a) {
         kernel<<<grid, threads, 0, a.stream>>>(a, rows, n, w);
         return launch_status();
       };
-      if (a.counts != nullptr) return a.fp32 ? run(ep_router_rows<true, true, L, V>) : run(ep_router_rows<false, true, L, V>);
-      return a.fp32 ? run(ep_router_rows<true, false, L, V>) : run(ep_router_rows<false, false, L, V>);
+      const auto with = [&](auto stats, auto places) {
+        constexpr bool S = decltype(stats)::value;
+        constexpr int KB = decltype(places)::value;
+        return a.fp32 ? run(ep_router_rows<true, S, L, V, KB>) : run(ep_router_rows<false, S, L, V, KB>);
+      };
+      constexpr std::integral_constant<int, 1> one{};
+      constexpr std::integral_constant<int, 64 / L> all{};
+      if (a.counts != nullptr) return a.K <= L ? with(std::true_type(), one) : with(std::true_type(), all);
+      return a.K <= L ? with(std::false_type(), one) : with(std::false_type(), all);
     });
     if (rc != 0) return rc;
   }
