@@ -153,16 +153,25 @@ __device__ __forceinline__ float terms(bool sigmoid, const float (&v)[V], float 
   return total;
 }
 
-// The sequence s with seq[s] <= t < seq[s + 1]: -1 before the first, S behind the last.
-__device__ __forceinline__ int sequence_of(const int32_t *seq, int S, int t) {
+// The sequence s with seq[s] <= t < seq[s + 1]: -1 before the first, S behind the last. L lanes look at L
+// of the remaining offsets at a time.
+template <int L>
+__device__ __forceinline__ int sequence_by_lanes(const int32_t *seq, int S, int t, int i) {
   if (seq == nullptr) return 0;
-  int lo = -1, hi = S + 1;  // seq[lo] <= t < seq[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (seq[mid] <= t) lo = mid;
-    else hi = mid;
+  int lo = 0, n = S + 1;  // the first lo offsets are at most t, those from lo + n on are not
+  while (ballot(n > 0) != 0) {
+    const int step = (n + L - 1) / L, at = lo + i * step;
+    const bool below = i * step < n && seq[i * step < n ? at : 0] <= t;
+    const int found = over_lanes<L>((int)below, [](int a, int b) { return a + b; });
+    const int left = n;
+    if (found == 0) {
+      n = 0;
+    } else {
+      const int skip = (found - 1) * step + 1;
+      lo += skip, n = left - skip < step - 1 ? left - skip : step - 1;
+    }
   }
-  return lo;
+  return lo - 1;
 }
 
 struct Slots {  // partial sums per (tile + sequence), then per sequence
@@ -343,8 +352,9 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_
     for (int pos = tile * tile_rows; pos < last;) {
       int s = 0, end = last;
       if (stats && a.seq != nullptr) {
-        s = sequence_of(a.seq, a.S, pos);
+        s = __builtin_amdgcn_readfirstlane(sequence_by_lanes<L>(a.seq, a.S, pos, i));
         if (s < a.S) end = a.seq[s + 1] < last ? a.seq[s + 1] : last;
+        if (end <= pos) end = pos + 1;  // offsets that do not ascend
       }
       const bool inside = STATS && s >= 0 && s < a.S;
       float acc[V], z = 0.f;
@@ -359,7 +369,11 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_
         const int row = first + group;
         const bool there = row < end, on = there && (a.mask == nullptr || a.mask[there ? row : pos] != 0);
         float v[V];
-        load_row<FP32, L, V>(a.logits, row, E, i, on, v);
+        load_row<FP32, L, V>(a.logits, row, E, i, there, v);  // whatever the mask says, which is still on its way
+        if (!on) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = -kInf;
+        }
         float top = -kInf, total = 0.f, ref = 0.f;
         float e[V];
         if (all_terms) {
@@ -630,26 +644,6 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
     if (a.balance != nullptr) *a.balance = v[2] > 0 ? (float)(v[0] / v[2]) : 0.f;
     if (a.z != nullptr) *a.z = v[3] > 0 ? (float)(v[1] / v[3]) : 0.f;
   }
-}
-
-// sequence_of by all of a row's lanes: L of the remaining offsets at a time.
-template <int L>
-__device__ __forceinline__ int sequence_by_lanes(const int32_t *seq, int S, int t, int i) {
-  if (seq == nullptr) return 0;
-  int lo = 0, n = S + 1;  // the first lo offsets are at most t, those from lo + n on are not
-  while (ballot(n > 0) != 0) {
-    const int step = (n + L - 1) / L, at = lo + i * step;
-    const bool below = i * step < n && seq[i * step < n ? at : 0] <= t;
-    const int found = over_lanes<L>((int)below, [](int a, int b) { return a + b; });
-    const int left = n;
-    if (found == 0) {
-      n = 0;
-    } else {
-      const int skip = (found - 1) * step + 1;
-      lo += skip, n = left - skip < step - 1 ? left - skip : step - 1;
-    }
-  }
-  return lo - 1;
 }
 
 // KB: places of a token's ids per lane.
