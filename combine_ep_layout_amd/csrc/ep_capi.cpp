@@ -909,6 +909,8 @@ int check_router(const char *what, int32_t T, int32_t E, int32_t K, int32_t S, i
                  int32_t scoring, float scale, const int32_t *seq_offsets, const int32_t *counts,
                  const int32_t *seq_tokens) {
   if (int rc = check_topk(what, T, K)) return rc;
+  if (T > INT32_MAX - 4096)
+    return fail(EP_EINVAL, "%s: num_tokens must be at most 2^31 - 4097 (got %d)", what, T);
   if (int rc = check_experts(what, E)) return rc;
   if (dtype != EP_BF16 && dtype != EP_FP32)
     return fail(EP_EINVAL, "%s: logits are bf16 or fp32 (got dtype %d)", what, dtype);

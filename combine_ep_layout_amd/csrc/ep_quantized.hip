@@ -1,5 +1,29 @@
 // The experts' products in 8-bit integers on the expand layout for gfx950:
 // y[r, n] = x_scales[r] * w_scales[e, n] * sum over k of x[r, k] w[e, n, k].
+//
+// Mathematics. Sums of products of two 8-bit integers are exact in the matrix cores' 32-bit
+// accumulators (32x32x32 and 16x16x64), in any order, and are scaled once at the end.
+//
+// Experts with more than 32 rows: 256 x 256 tiles, four waves of 128 x 128 results each (all 256 accumulator
+// registers), one workgroup a compute unit, which walks over its tiles without a pause: what comes next is loaded
+// straight into LDS two steps ahead, also across tiles, in steps of 128 values. What bounds it: the matrix
+// cores and the chip's power (1.5 GHz with normally distributed codes; zeros run at 2.3 GHz and are
+// no faster than the loads), next to the latency of HBM behind 64 KB of loads a compute unit.
+// What the measurements showed, each as the kernel stood:
+// - Whole lines. With 64 bytes of a row per load, a compute unit takes in 59 GB/s from L2, with 128 bytes 123 to
+//   130 (and 64 experts of 512 rows, 7168 to 4096, 1044 against 994 us).
+// - Loads between the products. A wave whose next load waits for the address unit issues no products: two
+//   loads for every four products instead of eight in a row, 8192^3 2142 against 2375 TOP/s.
+// - Scales through LDS beside the operands, not from memory at the tile's end (25 against 10 us a tile).
+// - A tile's blocks of 32 rows alternate between the waves, so that few rows are shared out evenly, and absent
+//   ones cost no products.
+// Measured on MI355X: 8192^3 458 us (2400 TOP/s; a large library product of the same codes 2184), 64 experts of
+// 512 rows 890 (2160), 8 of 2048 rows, 4096 to 2048, 127 to 130 (2100 to 2160).
+//
+// Experts with up to 32 rows: their weights are read once, which HBM bounds; see few_rows. 64 experts of
+// 8 rows, 7168 to 4096, 314 us (6.0 TB/s), of 32 rows 355; one row 8.4 us with the host's time (the kernel 8.8
+// under a trace). The border: 64 experts of 32 rows 355 us there and 380 in tiles, and with up to 128
+// rows in parts of 32 496 to 918 us against 386 to 435 in tiles.
 #include <type_traits>
 
 #include "ep_device.hpp"
@@ -42,7 +66,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
                : "memory");
 }
-// 4 bytes per lane to 256 bytes of LDS.
+// The same with 4 bytes per lane, for scales.
 __device__ __forceinline__ void touch(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
                : "memory");
@@ -57,6 +81,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 constexpr int kSide = 256, kBlock = 32, kBlocks = 4;
 constexpr int kOperandBytes = kSide * kStep, kStageBytes = 2 * kOperandBytes;  // of a step: x, then w
 constexpr int kLineOut = 128, kStrideOut = kLineOut + 16;  // results leave by lines of 32 rows
+
+__device__ __forceinline__ int tiles_of(int rows) { return rows / kSide + (rows % kSide != 0); }
 
 // The rows of expert e inside the buffer: their number, and the first in `begin`.
 __device__ __forceinline__ int span_of(const QuantizedMatmulArgs &a, int e, int &begin) {
@@ -111,7 +137,7 @@ __device__ __forceinline__ int expert_of(const int *before, int E, int v, int fr
 
 // Few rows: a workgroup takes RT * 16 channels of an expert with up to MT * 16 rows, its four waves a
 // quarter of the long axis each, through a ring of LDS of their own that no other wave waits for. The
-// rings run on from unit to unit; a unit's sums meet in LDS (integers: in any order).
+// rings run on from unit to unit, so that HBM never waits; a unit's sums meet in LDS (integers: in any order).
 constexpr int kFew = 32;              // rows
 constexpr int kRingBytes = 36 * 1024;  // of a wave
 constexpr int kScaleSlots = 9;         // units whose scales may be in LDS: one more than a ring has steps, and the one before
@@ -272,7 +298,7 @@ __device__ __forceinline__ Plan plan_of(const QuantizedMatmulArgs &a, int *lds) 
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     int b;
     const int n = span_of(a, e, b);
-    if (n > kFew) atomicAdd(&lds[0], (n + kSide - 1) / kSide * tiles_n);
+    if (n > kFew) atomicAdd(&lds[0], tiles_of(n) * tiles_n);
     else if (n > 0) atomicAdd(&lds[1], 1), atomicMax(&lds[2], n);
   }
   __syncthreads();
@@ -349,13 +375,13 @@ __global__ __launch_bounds__(kThreads, 1) void ep_quantized_matmul_tiles(const Q
   prefix_tiles(lds.before, lds.wave_sums, a.E, [&](int e) {
     int b;
     const int n = span_of(a, e, b);
-    return n > kFew ? (n + kSide - 1) / kSide * tiles_n : 0;
+    return n > kFew ? tiles_of(n) * tiles_n : 0;
   });
   // Unit v, for an expert that is not before `from`.
   const auto locate = [&](int v, int from) {
     Unit t{expert_of(lds.before, a.E, v, from), 0, 0, 0, 0};
     int begin;
-    const int count = __builtin_amdgcn_readfirstlane(span_of(a, t.e, begin)), tiles_m = (count + kSide - 1) / kSide;
+    const int count = __builtin_amdgcn_readfirstlane(span_of(a, t.e, begin)), tiles_m = tiles_of(count);
     const int i = v - __builtin_amdgcn_readfirstlane(lds.before[t.e]);
     if (i < 0 || i >= tiles_m * tiles_n) return t;  // spans that overlap so often that their tiles pass 2^31
     constexpr int kTall = 4;  // row tiles side by side before the next column tile

@@ -10,6 +10,16 @@
 // tokens: a tile of tokens keeps them in registers and leaves one partial sum
 // for each sequence that it meets in slot (tile + sequence), which no other
 // pair has, since both only grow; a second launch adds a sequence's slots in order.
+//
+// A row lies in 16 lanes (up to 256 experts; else in 64), so that a wave works on four at once and a
+// maximum over a row takes four DPP steps. What bounds it: for few tokens the launch (128 tokens of 256 experts,
+// 6.8 us under a trace, 8 with the host's time); for many the chain of a row's dependent steps, ten maxima of
+// which each needs the last, at four waves a SIMD. Measured on MI355X, 256 experts, top-8, fp32 logits:
+// 32768 tokens without statistics 15.0 us (softmax), 20.1 (sigmoid + bias); with them 36 and, in 37 packed
+// sequences, 47 (38 and 10 in the two launches); 4096 tokens 16.5. Backward 17 and 21 us, 131072 tokens 54
+// (5.0 TB/s, which is HBM). Steps: binary64 keys throughout 57 us for 128 tokens; statistics kept by workgroups of
+// 1024 threads, whose registers spill, 144 against 65 us; candidates ranked again one maximum at a time in
+// the rare near ties 77 against 20.6 us, since one such row holds up the launch.
 #include <type_traits>
 
 #include "ep_device.hpp"

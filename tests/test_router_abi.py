@@ -38,7 +38,7 @@ ROUTER = [dict(T=-1), dict(K=0), dict(K=65, E=128), dict(E=0), dict(E=1025), dic
           dict(given=1, bias=FAKE), dict(given=1, mask=FAKE), dict(c=None), dict(n=None), dict(c=None, n=None),
           dict(c=None, n=None, z=None), dict(sc=B.EP_SIGMOID), dict(l=None), dict(idx=None), dict(l=ODD), dict(ws=ODD),
           dict(ws=None), dict(wsb=16), dict(idx=FAKE + 2), dict(w=FAKE + 1), dict(bias=FAKE + 2), dict(seq=FAKE + 1, S=1),
-          dict(c=FAKE + 2), dict(n=FAKE + 2), dict(b=FAKE + 2), dict(z=FAKE + 2), dict(T=1 << 30, K=4)]
+          dict(c=FAKE + 2), dict(n=FAKE + 2), dict(b=FAKE + 2), dict(z=FAKE + 2), dict(T=1 << 30, K=4), dict(T=2 ** 31 - 1, K=1)]
 
 
 @pytest.mark.parametrize("kw", ROUTER, ids=str)
@@ -53,7 +53,7 @@ def backward(**kw):
     return tuple(a.values())
 
 
-BACKWARD = [dict(T=-1), dict(K=0), dict(K=65), dict(E=0), dict(E=1025), dict(S=0), dict(S=3), dict(dt=B.EP_FP4X2), dict(sc=5),
+BACKWARD = [dict(T=-1), dict(T=2 ** 31 - 1, K=1), dict(K=0), dict(K=65), dict(E=0), dict(E=1025), dict(S=0), dict(S=3), dict(dt=B.EP_FP4X2), dict(sc=5),
             dict(scale=float("nan")), dict(c=None), dict(n=None), dict(c=None, n=None), dict(c=None, n=None, db=None),
             dict(sc=B.EP_SIGMOID), dict(l=None), dict(idx=None), dict(d=None), dict(l=ODD), dict(d=FAKE + FAR + 4), dict(d=FAKE),
             dict(d=FAKE + 16), dict(idx=FAKE + 2), dict(dw=FAKE + 2), dict(db=FAKE + 1), dict(dz=FAKE + 2), dict(seq=FAKE + 2)]
