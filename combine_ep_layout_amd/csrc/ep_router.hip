@@ -15,8 +15,8 @@
 // maximum over a row takes four DPP steps. What bounds it: for few tokens the launch (128 tokens of 256 experts,
 // 6.8 us under a trace, 8 with the host's time); for many the chain of a row's dependent steps, ten maxima of
 // which each needs the last, at four waves a SIMD. Measured on MI355X, 256 experts, top-8, fp32 logits:
-// 32768 tokens without statistics 15.0 us (softmax), 20.1 (sigmoid + bias); with them 36 and, in 37 packed
-// sequences, 47 (38 and 10 in the two launches); 4096 tokens 16.5. Backward 17 and 21 us, 131072 tokens 54
+// 32768 tokens without statistics 15.2 us (softmax), 21 (sigmoid + bias); with them 33 and, in 37 packed
+// sequences, 45 (36 and 10 in the two launches); 4096 tokens 16.5. Backward 17 and 21 us, 131072 tokens 54
 // (5.0 TB/s, which is HBM). Steps: binary64 keys throughout 57 us for 128 tokens; statistics kept by workgroups of
 // 1024 threads, whose registers spill, 144 against 65 us; candidates ranked again one maximum at a time in
 // the rare near ties 77 against 20.6 us, since one such row holds up the launch.
@@ -208,9 +208,11 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // Fast: a key's upper bits and its column (descending) in one 31-bit number, so that a maximum is one integer
 // instruction and names its column; x - m, as an unsigned number, puts what is still below the last
 // maximum m on top. bf16 logits fit whole. Of binary32 keys the lower bits are lost: then K + 2
-// candidates are taken and ranked by their whole keys, and the choice stands if what was
-// left out lies below the K-th whatever its lower bits are. Candidates' scores + bias that differ by no more
-// than their rounding errors (one row in a thousand) are ranked again in binary64.
+// candidates (K + 4 of scores + bias) are taken and ranked by their whole keys, and the choice stands if what
+// was left out lies below the K-th whatever its lower bits are. Candidates' scores + bias that differ by no
+// more than their rounding errors (one row in a thousand) are ranked again in binary64. With K + 2 of them one
+// batch of 32768 tokens in two has a row that needs the exact choice, which holds up the launch (packed batch
+// 44 us without such a row, 56 to 90 with one); K + 4 cost 1 us and leave none.
 // Exact: binary64 keys, one maximum at a time; for rows where what is left out may reach the K-th (many
 // equal keys), and for more candidates than lanes.
 template <int L, int V>
@@ -341,8 +343,11 @@ struct Chooser {
   }
 };
 
+constexpr int kMostOf16 = 256;                // experts of a row in 16 lanes
+constexpr int kPerUnit16 = 3, kPerUnit64 = 4;  // workgroups with statistics on a compute unit, as registers allow
+
 template <bool FP32, bool STATS, int L, int V, int KB>
-__global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
+__global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit64) void ep_router_rows(const RouterArgs a, int tile_rows, int tiles,
                                                               Slots out) {
   using Choice = Chooser<L, V>;
   constexpr int kWaves = kThreads / kWave;
@@ -353,7 +358,8 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? 3 : 4) void ep_router_
   const int i = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L, E = a.E, K = a.K;
   constexpr bool stats = STATS;
   const bool packed_whole = !FP32 && a.bias == nullptr;  // no key bits are lost
-  const int candidates = packed_whole ? K : (K + 2 < E ? K + 2 : E);
+  const int wish = a.bias != nullptr && K + 4 <= L ? K + 4 : K + 2;
+  const int candidates = packed_whole ? K : (wish < E ? wish : E);
   const bool fast = candidates <= L;
   const bool all_terms = stats || a.bias != nullptr || !(a.normalize || a.sigmoid);
   if (stats && blockIdx.x == 0 && threadIdx.x == 0) *out.done = 0;  // for the next launch
@@ -829,11 +835,13 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
   }
 }
 
-// Tokens per tile, and so per slot: 16 as long as that leaves about a thousand tiles, at most 256.
-int tile_rows_of(int T) {
-  int rows = 16;
-  while (rows < 256 && T / rows > 1024) rows *= 2;
-  return rows;
+// Tokens per tile, and so per slot: as few sixteens as leave no more tiles than workgroups run at once, three
+// or four a compute unit (powers of two up to 1024 tiles: 32768 tokens of 256 experts 36 us instead of 32.6,
+// 131072 95 instead of 85; 768 tiles of 1024 experts 116 instead of 106), and at most 256.
+int tile_rows_of(int T, int E) {
+  const int at_once = (E <= kMostOf16 ? kPerUnit16 : kPerUnit64) * 256;
+  const int64_t sixteens = ((int64_t)T + 16 * at_once - 1) / (16 * at_once);
+  return 16 * (int)(sixteens < 1 ? 1 : (sixteens < 16 ? sixteens : 16));
 }
 
 // Columns per workgroup of the second launch: the fewer, the more slots a sequence has.
@@ -848,7 +856,7 @@ struct Sizes {
 };
 Sizes sizes_of(int T, int E, int S) {
   Sizes z;
-  z.tile_rows = tile_rows_of(T);
+  z.tile_rows = tile_rows_of(T, E);
   z.tiles = (int)(((int64_t)T + z.tile_rows - 1) / z.tile_rows);
   z.slots = (int64_t)z.tiles + S;
   z.lanes = lanes_of(z.tiles, S);
@@ -865,7 +873,7 @@ int for_shape(int E, F f) {
   if (E <= 32) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
   if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
   if (E <= 128) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
-  if (E <= 256) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+  if (E <= kMostOf16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
   if (E <= 512) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
   return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
 }

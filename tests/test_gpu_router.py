@@ -196,6 +196,25 @@ def test_keys_that_binary32_cannot_tell_apart(scoring):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(12, 8), (40, 8), (256, 8), (256, 13), (600, 8), (600, 40)])
+def test_neighbours_around_the_last_place(E, K, scoring):
+    """Row n has n keys within a few steps of each other around the K-th place, the rest far away."""
+    _say(f"[neighbours] E={E} K={K} {scoring}")
+    gen = _gen(6, E, K)
+    T = min(E, 70)
+    l = torch.randn(T, E, generator=gen, device=DEV)
+    for n in range(T):
+        at = torch.randperm(E, generator=gen, device=DEV)
+        above = max(0, min(K - 1 - n // 2, E - n))
+        l[n, at[:above]] += 9.0
+        steps = torch.randint(0, 40, (n,), generator=gen, device=DEV).to(torch.int32)
+        l[n, at[above:above + n]] = (torch.full((n,), 5.0, device=DEV).view(torch.int32) + steps).view(torch.float32)
+    Forward(l, K, scoring)().check()
+    Forward(l, K, scoring, bias=torch.zeros(E, device=DEV))().check()
+    Forward(l, K, scoring, bias=torch.randint(0, 2, (E,), generator=gen, device=DEV).float())().check()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("E", [40, 256, 600])
 def test_extreme_logits(E, kind, scoring):
