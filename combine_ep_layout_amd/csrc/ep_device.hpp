@@ -118,29 +118,6 @@ __device__ __forceinline__ int clip_span(int &begin, int count, int64_t capacity
   return (int)(end - begin);
 }
 
-// Bit r set: row r0 + r (r < n <= 32) lies in some expert's span. All threads
-// of the workgroup call it.
-template <int THREADS>
-__device__ __forceinline__ uint32_t real_rows(const int32_t *__restrict__ counts,
-                                              const int32_t *__restrict__ offsets, int E, int64_t r0,
-                                              int n, uint32_t *lds) {
-  const uint32_t all = n == 32 ? ~0u : (1u << n) - 1;
-  if (counts == nullptr) return all;
-  __syncthreads();
-  if (threadIdx.x == 0) *lds = 0;
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += THREADS) {
-    const int64_t b = offsets[e], end = b + counts[e];
-    const int64_t lo = b > r0 ? b : r0, hi = end < r0 + n ? end : r0 + n;
-    if (lo < hi) {
-      const int len = (int)(hi - lo);
-      atomicOr(lds, (len == 32 ? ~0u : (1u << len) - 1) << (int)(lo - r0));
-    }
-  }
-  __syncthreads();
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)*lds);
-}
-
 // Sum over the 64 lanes of a wavefront (the same value in every lane).
 __device__ __forceinline__ int wave_sum(int x) {
   x = row_inclusive_scan(x);

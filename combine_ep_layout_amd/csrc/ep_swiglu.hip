@@ -154,6 +154,28 @@ __device__ __forceinline__ void dequantize(u32x2 codes, float scale, float (&v)[
   }
 }
 
+// Bit r set: row r0 + r (r < n <= 32) lies in some expert's span. All threads
+// of the workgroup call it.
+__device__ __forceinline__ uint32_t real_rows(const int32_t *__restrict__ counts,
+                                              const int32_t *__restrict__ offsets, int E, int64_t r0,
+                                              int n, uint32_t *lds) {
+  const uint32_t all = n == 32 ? ~0u : (1u << n) - 1;
+  if (counts == nullptr) return all;
+  __syncthreads();
+  if (threadIdx.x == 0) *lds = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    const int64_t b = offsets[e], end = b + counts[e];
+    const int64_t lo = b > r0 ? b : r0, hi = end < r0 + n ? end : r0 + n;
+    if (lo < hi) {
+      const int len = (int)(hi - lo);
+      atomicOr(lds, (len == 32 ? ~0u : (1u << len) - 1) << (int)(lo - r0));
+    }
+  }
+  __syncthreads();
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)*lds);
+}
+
 template <bool FP32, bool SAVE>
 __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
     const char *__restrict__ gate_up, const int32_t *__restrict__ counts,
@@ -166,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_rows(
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t r0 = b * block_rows;
     const int n = (int)(capacity - r0 < block_rows ? capacity - r0 : block_rows);
-    const uint32_t real = real_rows<kThreads>(counts, offsets, E, r0, n, &lds);
+    const uint32_t real = real_rows(counts, offsets, E, r0, n, &lds);
     if (real == 0) continue;
     const __amdgpu_buffer_rsrc_t to_h = rows_of(h, r0, n, (int64_t)I * kElt);
     const __amdgpu_buffer_rsrc_t to_codes = SAVE ? rows_of(codes, r0, n, 2 * (int64_t)I) : to_h;
@@ -212,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void ep_swiglu_backward_rows(
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t r0 = b * block_rows;
     const int n = (int)(capacity - r0 < block_rows ? capacity - r0 : block_rows);
-    const uint32_t real = real_rows<kThreads>(counts, offsets, E, r0, n, &lds);
+    const uint32_t real = real_rows(counts, offsets, E, r0, n, &lds);
     if (real == 0) continue;
     const __amdgpu_buffer_rsrc_t to_d = rows_of(d_gate_up, r0, n, 2 * (int64_t)I * kElt);
     const __amdgpu_buffer_rsrc_t to_h = WITH_H ? rows_of(h, r0, n, (int64_t)I * kElt) : to_d;

@@ -408,6 +408,40 @@ def test_quantize_spans_that_leave_the_buffer_are_cut(counts, offsets):
     assert bool((whole[~real] == 99).all()) and bool((scales[~real] == -7.0).all())
 
 
+@pytest.mark.parametrize("E,W,kind,rows", [(1024, 32, "fp32", 90000), (300, 2064, "bf16", 14000), (70, 20000, "bf16", 3500), (256, 512, "bf16", 40000)])
+def test_quantize_many_ragged_experts(E, W, kind, rows):
+    """More rows than workgroups take at once, experts in no order, some of them without rows, padding between."""
+    _say(f"[quantize many] E={E} W={W} {kind} rows={rows}")
+    gen = _gen(14, E, W)
+    share = torch.rand(E, generator=gen, device=DEV) ** 3
+    share[torch.rand(E, generator=gen, device=DEV) < 0.3] = 0
+    counts = (share / share.sum() * rows).to(torch.int32)
+    order = torch.randperm(E, generator=gen, device=DEV)
+    room = (counts[order] + 40 + 7) // 8 * 8
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[order] = (torch.cumsum(room, 0) - room).to(torch.int32)
+    cap = int(room.sum())
+    real = torch.zeros(cap, dtype=torch.bool, device=DEV)
+    for b, n in zip(offsets.tolist(), counts.tolist()):
+        real[b:b + n] = True
+    x = torch.randn(cap, W, generator=gen, device=DEV).to(TYPE[kind])
+    x[~real] = NAN
+    want, scale = _quantized(x[real].float())
+    for limit in (0, 3):
+        codes = torch.full((cap, W), 99, dtype=torch.int8, device=DEV)
+        scales = torch.full((cap, 1), -7.0, device=DEV)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        if limit:
+            B.ep_set_workgroup_limit(s, limit)
+        B.ep_quantize_rows(x, counts, offsets, E, cap, W, KIND[kind], codes, scales, 1, s)
+        s.synchronize()
+        if limit:
+            B.ep_set_workgroup_limit(s, 0)
+        assert torch.equal(codes[real], want) and torch.equal(scales[real][:, 0], scale)
+        assert bool((codes[~real] == 99).all()) and bool((scales[~real] == -7.0).all())
+
+
 def test_quantize_behind_4_gib():
     R, W = (1 << 20) + 70, 4096  # codes just over 4 GiB
     _say(f"[quantize large] {R} x {W}")
