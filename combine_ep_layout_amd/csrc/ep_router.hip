@@ -250,6 +250,10 @@ struct Chooser {
     return mine;
   }
   static __device__ __forceinline__ int column_of(uint32_t packed) { return (int)(kColumns - (packed & kColumns)); }
+  // The key, if its lower bits are zeros.
+  static __device__ __forceinline__ float whole(uint32_t packed) {
+    return __uint_as_float(__float_as_uint(unordered(packed >> kColumnBits << kLost)) >> kLost << kLost);
+  }
   // A number that no key with this packed number exceeds.
   static __device__ __forceinline__ float at_most(uint32_t packed) {
     return unordered(packed >> kColumnBits << kLost | ((1u << kLost) - 1));
@@ -400,6 +404,8 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
           total = lanes_sum<L>(terms(a.sigmoid, v, ref, e));
         }
         int ids[KB], places[KB];  // of this lane
+        float chosen = -kInf;     // logit of ids[0], if `known`
+        bool known = false;
 #pragma unroll
         for (int b = 0; b < KB; ++b) places[b] = b * L + i, ids[b] = -1;
         if (!a.given) {
@@ -419,10 +425,13 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
             const uint32_t mine = Choice::largest(x, candidates, i);
             const bool valid = mine != 0 && i < candidates;
             ids[0] = valid ? Choice::column_of(mine) : -1;
-            if (!packed_whole) {
+            known = true;
+            if (packed_whole) {
+              chosen = Choice::whole(mine);
+            } else {
               float key = -kInf, near = -1.0f;
               if (valid) {
-                key = load_one<FP32>(a.logits, (int64_t)row * E + ids[0]);
+                key = chosen = load_one<FP32>(a.logits, (int64_t)row * E + ids[0]);
                 if (a.bias != nullptr) {
                   // errors of scores: 16 * 2^-23 for sigmoids; 128 * 2^-23 of the largest probability
                   const float most = fabsf(Choice::at_most(mine));
@@ -447,7 +456,7 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
                 }
                 double exact = -(double)kInf;
                 if (valid) {
-                  const double l = load_one<FP32>(a.logits, (int64_t)row * E + ids[0]);
+                  const double l = chosen;
                   exact = (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)ref) / sum) + (double)a.bias[ids[0]];
                 }
                 places[0] = Choice::rank(exact, valid ? ids[0] : E + i, candidates, near, close);
@@ -457,6 +466,7 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
           }
           unsure = lanes_any<L>(unsure && there);
           if (ballot(unsure) != 0) {
+            known = false;
             int exact[KB];
             Choice::template exactly<FP32, KB>(a, row, on, ref, i, exact);
             if (unsure) {
@@ -478,7 +488,8 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
           if (ids[b] >= 0 && !there) ids[b] = -1;
-          l[b] = ids[b] >= 0 ? load_one<FP32>(a.logits, (int64_t)row * E + ids[b]) : -kInf;
+          l[b] = -kInf;
+          if (ids[b] >= 0) l[b] = known && b == 0 ? chosen : load_one<FP32>(a.logits, (int64_t)row * E + ids[b]);
           most = fmaxf(most, l[b]);
           any |= ids[b] >= 0;
         }
