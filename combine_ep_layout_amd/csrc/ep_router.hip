@@ -650,7 +650,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
   }
   if (threadIdx.x == 0) {
     // What this thread has published has left for all when its stores are done; there is nothing else to hand
-    // over, so no write-back of L2 (10.3 instead of 7.6 us for 37 sequences).
+    // over, so no write-back of L2 (which takes 2.7 of 10.3 us for 37 sequences).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     last = __hip_atomic_fetch_add(in.done, (unsigned)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + (unsigned)mine == (unsigned)units;
   }
