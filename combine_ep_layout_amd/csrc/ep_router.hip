@@ -782,8 +782,10 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (!a.sigmoid && !a.normalize) {
       dot = lanes_sum<L>(dot);
+      if (any) {  // else out is 0, and p may be of anything: a row of padding
 #pragma unroll
-      for (int j = 0; j < V; ++j) out[j] = p[j] * (out[j] - dot);
+        for (int j = 0; j < V; ++j) out[j] = p[j] * (out[j] - dot);
+      }
     }
     if (any && s >= 0 && s < a.S) {
       if (a.d_balance != nullptr) {
