@@ -957,7 +957,7 @@ size_t ep_router_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_
     if (num_tokens < 0 || num_experts < 1 || num_experts > EP_MAX_EXPERTS || num_sequences < 1 ||
         num_sequences > EP_MAX_SEQUENCES)
       return 0;
-    return ep::router_workspace(num_tokens, num_experts, num_sequences);
+    return ep::router_workspace_most(num_tokens, num_experts, num_sequences);
   } catch (...) {
     return 0;
   }

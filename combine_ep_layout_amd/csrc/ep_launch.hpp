@@ -333,7 +333,8 @@ int launch_swiglu(const SwigluArgs &a);
 int launch_swiglu_backward(const SwigluBackwardArgs &a);
 int launch_expert_wgrad(const ExpertWgradArgs &a);
 int launch_router(const RouterArgs &a);
-size_t router_workspace(int T, int E, int S);
+size_t router_workspace(int T, int E, int S);       // what this call needs
+size_t router_workspace_most(int T, int E, int S);  // what no smaller call exceeds
 int launch_router_backward(const RouterBackwardArgs &a);
 int launch_quantize(const QuantizeArgs &a);
 int launch_quantized_matmul(const QuantizedMatmulArgs &a);

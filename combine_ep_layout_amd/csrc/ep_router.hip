@@ -852,16 +852,19 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
 // Tokens per tile, and so per slot: as few sixteens as leave no more tiles than workgroups run at once, three
 // or four a compute unit (powers of two up to 1024 tiles: 32768 tokens of 256 experts 36 us instead of 32.6,
 // 131072 95 instead of 85; 768 tiles of 1024 experts 116 instead of 106), and at most 256.
+constexpr int kMostSixteens = 16;
+int tiles_at_once(int E) { return (E <= kMostOf16 ? kPerUnit16 : kPerUnit64) * 256; }
 int tile_rows_of(int T, int E) {
-  const int at_once = (E <= kMostOf16 ? kPerUnit16 : kPerUnit64) * 256;
+  const int at_once = tiles_at_once(E);
   const int64_t sixteens = ((int64_t)T + 16 * at_once - 1) / (16 * at_once);
-  return 16 * (int)(sixteens < 1 ? 1 : (sixteens < 16 ? sixteens : 16));
+  return 16 * (int)(sixteens < 1 ? 1 : (sixteens < kMostSixteens ? sixteens : kMostSixteens));
 }
 
 // Columns per workgroup of the second launch: the fewer, the more slots a sequence has.
+constexpr int kManySlots = 256, kSomeSlots = 64;
 int lanes_of(int64_t tiles, int S) {
   const int64_t slots = tiles / S;
-  return slots >= 256 ? 4 : (slots >= 64 ? 16 : 64);
+  return slots >= kManySlots ? 4 : (slots >= kSomeSlots ? 16 : 64);
 }
 
 struct Sizes {
@@ -880,6 +883,10 @@ Sizes sizes_of(int T, int E, int S) {
 
 int64_t up(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
+size_t workspace_of(int64_t slots, int E, int S, int64_t terms) {
+  return (size_t)(2 * up(slots * E * 4) + 2 * up(slots * 4) + up(terms * 8) + up((int64_t)S * 8) + up(4));
+}
+
 // f(L, V) for the smallest row of L lanes with V values each that holds E logits.
 template <class F>
 int for_shape(int E, F f) {
@@ -896,7 +903,22 @@ int for_shape(int E, F f) {
 
 size_t router_workspace(int T, int E, int S) {
   const Sizes z = sizes_of(T, E, S);
-  return (size_t)(2 * up(z.slots * E * 4) + 2 * up(z.slots * 4) + up((int64_t)S * z.parts * 8) + up((int64_t)S * 8) + up(4));
+  return workspace_of(z.slots, E, S, (int64_t)S * z.parts);
+}
+
+// What no call of at most T tokens, E experts and S sequences exceeds. Tiles jump down where their rows go up by
+// 16, and terms of the losses where sequences get fewer slots, so a call may need less than a smaller one.
+size_t router_workspace_most(int T, int E, int S) {
+  const int64_t sixteens = ((int64_t)T + 15) / 16, at_once = tiles_at_once(E);
+  const int64_t tall = (sixteens + kMostSixteens - 1) / kMostSixteens, some = at_once > tall ? at_once : tall;
+  const int64_t tiles = sixteens < some ? sixteens : some;
+  int64_t terms = 0;
+  for (const int lanes : {4, 16, 64}) {  // of as many sequences as get so few columns a workgroup
+    const int64_t most = lanes == 64 ? S : tiles / (lanes == 4 ? kManySlots : kSomeSlots);
+    const int64_t n = (most < S ? most : S) * ((E + lanes - 1) / lanes);
+    terms = n > terms ? n : terms;
+  }
+  return workspace_of(tiles + S, E, S, terms);
 }
 
 int launch_router(const RouterArgs &a) {

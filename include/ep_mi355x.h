@@ -590,7 +590,9 @@ int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const 
 
 /*
  * Bytes of device workspace ep_router needs for counts and losses: partial
- * sums per tile of tokens and sequence. 0 for out-of-range arguments.
+ * sums per tile of tokens and sequence. 0 for out-of-range arguments. Never
+ * fewer for more tokens, experts or sequences: a buffer for the largest call
+ * serves every smaller one.
  * Scratch: its contents on entry do not matter; two calls in flight at once
  * (two streams, two graphs that may replay together) must not share one.
  */
