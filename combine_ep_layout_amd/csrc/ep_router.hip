@@ -214,7 +214,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // batch of 32768 tokens in two has a row that needs the exact choice, which holds up the launch (packed batch
 // 44 us without such a row, 56 to 90 with one); K + 4 cost 1 us and leave none.
 // Exact: binary64 keys, one maximum at a time; for rows where what is left out may reach the K-th (many
-// equal keys), and for more candidates than lanes.
+// equal keys), for softmax + bias of rows that hold NaN or +infinity, and for more candidates than lanes.
 template <int L, int V>
 struct Chooser {
   static constexpr int kColumnBits = (L * V <= 16 ? 4 : L * V <= 32 ? 5 : L * V <= 64 ? 6 : L * V <= 128 ? 7 : L * V <= 256 ? 8 : L * V <= 512 ? 9 : 10);
@@ -303,13 +303,16 @@ struct Chooser {
   // maximum instead of keeping binary64 keys in registers.
   template <bool FP32, int KB>
   static __device__ __forceinline__ void exactly(const RouterArgs &a, int64_t row, bool on, float ref, int i, int (&ids)[KB]) {
+    // softmax's term; `ref` is infinite if the row's largest logit is
+    const auto part = [&](float l) { return ref == kInf ? (double)(l == kInf) : exp((double)l - (double)ref); };
     double sum = 1.0;
     if (a.bias != nullptr && !a.sigmoid) {
       sum = 0.0;
 #pragma unroll 1
       for (int j = 0; j < V; ++j) {
         const int c = column<L, V>(i, j);
-        if (on && c < a.E) sum += exp((double)load_one<FP32>(a.logits, row * a.E + c) - (double)ref);
+        const float l = on && c < a.E ? load_one<FP32>(a.logits, row * a.E + c) : -kInf;
+        if (l > -kInf) sum += part(l);
       }
 #pragma unroll
       for (int d = 1; d < L; d *= 2) sum += __shfl_xor(sum, d);
@@ -330,7 +333,7 @@ struct Chooser {
           if (!(l > -kInf)) continue;
           double key = l;
           if (a.bias != nullptr)
-            key = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)ref) / sum) + (double)a.bias[c];
+            key = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : part(l) / sum) + (double)a.bias[c];
           // what comes behind the last one, and before the best so far
           if ((key < last || (key == last && c > last_at)) && key > best) best = key, at = c;
         }
@@ -462,6 +465,7 @@ __global__ __launch_bounds__(kThreads, STATS && L == 16 ? kPerUnit16 : kPerUnit6
                 places[0] = Choice::rank(exact, valid ? ids[0] : E + i, candidates, near, close);
               }
               if (places[0] >= K) ids[0] = -1;
+              if (a.bias != nullptr && !a.sigmoid) unsure |= total != total;  // NaN or +infinity among the logits: no keys
             }
           }
           unsure = lanes_any<L>(unsure && there);

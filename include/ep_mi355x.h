@@ -607,8 +607,11 @@ size_t ep_router_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_
  * lowest id first. s + bias is compared as if without rounding errors: sums
  * that binary32 cannot tell apart are computed again in binary64. An expert whose
  * logit is -infinity or NaN, or whose bias is -infinity or NaN, is not chosen; where no
- * more are left, and for a token whose token_mask is 0, the id is -1. Then, for
- * every id in [0, num_experts) of a token
+ * more are left, and for a token whose token_mask is 0, the id is -1. A NaN logit
+ * leaves out no other expert: for the choice the others' scores are those of the row
+ * without it, and experts at +infinity share a softmax score of 1. (Weights and losses
+ * follow their formulas: NaN where a sum over the row, or a chosen logit, makes it so.)
+ * Then, for every id in [0, num_experts) of a token
  *   topk_weights[t, k] = scale * s_i                          (normalize = 0)
  *                      = scale * s_i / sum over the token's ids of s_j  (else)
  * and 0 for other ids. With given != 0, topk_idx is an input instead (ids
