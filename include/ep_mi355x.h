@@ -629,8 +629,8 @@ size_t ep_router_workspace_bytes(int32_t num_tokens, int32_t num_experts, int32_
  *   z_loss         = mean over the n tokens of (log sum over e of exp(l_e))^2
  * Losses of no tokens are 0. With one sequence, counts are ep_layout's.
  * Scores in binary32 (exponentials below 2^-126 may count as 0); sums over tokens in binary32 over at most 256 tokens, and
- * in binary64 beyond. A token whose logits are all -infinity (or none of whose
- * chosen ones is above) has p = 0, weights 0 and log sum 0.
+ * in binary64 beyond. A token none of whose ids' logits is above -infinity has
+ * weights 0; one whose logits are all -infinity has p = 0 and log sum 0 too.
  *
  *   logits         [num_tokens, num_experts] of dtype (EP_BF16, EP_FP32)
  *   select_bias    fp32 [num_experts] or NULL; not with given
