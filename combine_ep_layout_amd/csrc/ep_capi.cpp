@@ -11,6 +11,7 @@
 
 #include <atomic>
 #include <exception>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -905,6 +906,29 @@ int ep_expert_wgrad(const void *dy, const void *x, const float *x_scales, const 
 
 namespace {
 
+// An operand's bytes, if it has any.
+struct Operand {
+  const char *name;
+  const void *p;
+  int64_t bytes;
+};
+
+// No result may share a byte with another result or with an operand that is read.
+int check_apart(const char *what, std::initializer_list<Operand> results,
+                std::initializer_list<Operand> read) {
+  const auto shared = [](const Operand &a, const Operand &b) {
+    return a.bytes > 0 && b.bytes > 0 && overlap(a.p, a.bytes, b.p, b.bytes);
+  };
+  for (const Operand *a = results.begin(); a != results.end(); ++a) {
+    for (const Operand *b = a + 1; b != results.end(); ++b)
+      if (shared(*a, *b))
+        return fail(EP_EINVAL, "%s: %s and %s overlap", what, a->name, b->name);
+    for (const Operand &b : read)
+      if (shared(*a, b)) return fail(EP_EINVAL, "%s: %s overlaps %s", what, a->name, b.name);
+  }
+  return EP_OK;
+}
+
 int check_router(const char *what, int32_t T, int32_t E, int32_t K, int32_t S, int32_t dtype,
                  int32_t scoring, float scale, const int32_t *seq_offsets, const int32_t *counts,
                  const int32_t *seq_tokens) {
@@ -1108,6 +1132,15 @@ int ep_quantized_matmul(const void *x, const float *x_scales, int32_t x_scale_co
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(x_scales, 4) ||
         !aligned(w_scales, 4))
       return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
+    const int64_t E = num_experts, cap = capacity_rows, K = in_features, N = out_features;
+    if (int rc = check_apart(what, {{"y", y, cap * N * (y_dtype == EP_FP32 ? 4 : 2)}},
+                             {{"x", x, cap * K},
+                              {"x_scales", x_scales, cap > 0 ? ((cap - 1) * x_scale_cols + 1) * 4 : 0},
+                              {"w", w, E * N * K},
+                              {"w_scales", w_scales, E * N * 4},
+                              {"counts", counts, E * 4},
+                              {"offsets", offsets, E * 4}}))
+      return rc;
     ep::QuantizedMatmulArgs a{x, x_scales, x_scale_cols, w, w_scales, counts, offsets, num_experts,
                               capacity_rows, in_features, out_features, y, y_dtype == EP_FP32,
                               (hipStream_t)stream};
