@@ -955,7 +955,8 @@ int check_router(const char *what, int32_t T, int32_t E, int32_t K, int32_t S, i
 
 // Rows of int8 codes, `width` values each, and their scales.
 int check_codes(const char *what, int32_t width, int32_t dtype, const void *x, const void *codes,
-                const float *scales, int32_t scale_cols, int64_t capacity_rows, int factor) {
+                const float *scales, int32_t scale_cols, const int32_t *counts,
+                const int32_t *offsets, int32_t num_experts, int64_t capacity_rows, int factor) {
   if (int rc = check_row_dtype(what, dtype)) return rc;
   if (width < 16 || width % 16 != 0 || width > (1 << 24))
     return fail(EP_EINVAL, "%s: rows must be a positive multiple of 16 values up to 2^24 (got %d)",
@@ -966,10 +967,11 @@ int check_codes(const char *what, int32_t width, int32_t dtype, const void *x, c
     return fail(EP_EINVAL, "%s: a required pointer is NULL", what);
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
     return fail(EP_EINVAL, "%s: misaligned pointer (rows need 16 bytes)", what);
-  const int64_t bytes = capacity_rows * width;
-  if (overlap(codes, bytes, x, bytes * factor * (dtype == EP_FP32 ? 4 : 2)))
-    return fail(EP_EINVAL, "%s: the codes must not overlap their input", what);
-  return EP_OK;
+  const int64_t bytes = capacity_rows * width, E = num_experts;
+  return check_apart(what, {{"codes", codes, bytes}, {"scales", scales, capacity_rows * scale_cols * 4}},
+                     {{factor == 2 ? "gate_up" : "x", x, bytes * factor * (dtype == EP_FP32 ? 4 : 2)},
+                      {"counts", counts, E * 4},
+                      {"offsets", offsets, E * 4}});
 }
 
 }  // namespace
@@ -1074,7 +1076,8 @@ int ep_quantize_rows(const void *x, const int32_t *counts, const int32_t *offset
     const char *what = "ep_quantize_rows";
     discard_stale_error();
     if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
-    if (int rc = check_codes(what, width, dtype, x, codes, scales, scale_cols, capacity_rows, 1))
+    if (int rc = check_codes(what, width, dtype, x, codes, scales, scale_cols, counts, offsets,
+                             num_experts, capacity_rows, 1))
       return rc;
     ep::QuantizeArgs a{x, counts, offsets, num_experts, capacity_rows, width, dtype == EP_FP32,
                        false, codes, scales, scale_cols, (hipStream_t)stream};
@@ -1094,8 +1097,8 @@ int ep_swiglu_quantize(const void *gate_up, const int32_t *counts, const int32_t
     const char *what = "ep_swiglu_quantize";
     discard_stale_error();
     if (int rc = check_segments(what, counts, offsets, num_experts, capacity_rows)) return rc;
-    if (int rc = check_codes(what, intermediate, dtype, gate_up, codes, scales, scale_cols,
-                             capacity_rows, 2))
+    if (int rc = check_codes(what, intermediate, dtype, gate_up, codes, scales, scale_cols, counts,
+                             offsets, num_experts, capacity_rows, 2))
       return rc;
     ep::QuantizeArgs a{gate_up, counts, offsets, num_experts, capacity_rows, intermediate,
                        dtype == EP_FP32, true, codes, scales, scale_cols, (hipStream_t)stream};

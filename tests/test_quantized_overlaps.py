@@ -55,3 +55,26 @@ def test_matmul_results_beside_an_operand_are_not_refused(name):
     _no_gpu()
     for y in (PLACE[name] + (BYTES[name] + 15) // 16 * 16, PLACE[name] - CAP * N * 4):
         assert not _refused(B.ep_quantized_matmul, matmul(y=y))
+
+
+def quantize(**at):
+    p = {**PLACE, **at}
+    return p["x"], p["c"], p["o"], E, CAP, K, B.EP_FP32, p["codes"], p["s"], COLS
+
+
+@pytest.mark.parametrize("fn,factor", [(B.ep_quantize_rows, 1), (B.ep_swiglu_quantize, 2)], ids=["rows", "gated"])
+@pytest.mark.parametrize("name", ["x", "codes", "c", "o"])
+def test_scales_over_an_operand(fn, factor, name):
+    size = {"x": CAP * K * 4 * factor, "codes": CAP * K, "c": E * 4, "o": E * 4}[name]
+    for at in (0, size - 4, 4 - CAP * COLS * 4):
+        assert _refused(fn, quantize(s=PLACE[name] + at)), at
+    if name != "codes":
+        for at in (0, size - 4, 16 - CAP * K):
+            assert _refused(fn, quantize(codes=PLACE[name] + at // 16 * 16)), at
+
+
+@pytest.mark.parametrize("fn,factor", [(B.ep_quantize_rows, 1), (B.ep_swiglu_quantize, 2)], ids=["rows", "gated"])
+def test_scales_beside_an_operand_are_not_refused(fn, factor):
+    _no_gpu()
+    for s in (PLACE["x"] + CAP * K * 4 * factor, PLACE["codes"] + CAP * K, PLACE["codes"] - CAP * COLS * 4, PLACE["c"] + 4 * E):
+        assert not _refused(fn, quantize(s=s))
