@@ -1015,12 +1015,27 @@ int ep_router(const void *logits, const float *select_bias, const uint8_t *token
         !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(balance_loss, 4) ||
         !aligned(z_loss, 4))
       return fail(EP_EINVAL, "%s: misaligned pointer (logits and the workspace need 16 bytes)", what);
+    size_t need = 0;
     if (counts != nullptr) {
-      const size_t need = ep::router_workspace(num_tokens, num_experts, num_sequences);
+      need = ep::router_workspace(num_tokens, num_experts, num_sequences);
       if (!workspace || workspace_bytes < need)
         return fail(EP_EINVAL, "%s: workspace of %zu bytes needed (got %zu)", what, need,
                     workspace ? workspace_bytes : (size_t)0);
     }
+    const int64_t T = num_tokens, E = num_experts, S = num_sequences, entries = T * topk * 4;
+    if (int rc = check_apart(what, {{"topk_idx", topk_idx, given ? 0 : entries},
+                                    {"topk_weights", topk_weights, entries},
+                                    {"counts", counts, S * E * 4},
+                                    {"seq_tokens", seq_tokens, (S + 2) * 4},
+                                    {"balance_loss", balance_loss, 4},
+                                    {"z_loss", z_loss, 4},
+                                    {"workspace", workspace, (int64_t)need}},
+                             {{"logits", logits, T * E * (dtype == EP_FP32 ? 4 : 2)},
+                              {"topk_idx", topk_idx, given ? entries : 0},
+                              {"select_bias", select_bias, E * 4},
+                              {"token_mask", token_mask, T},
+                              {"seq_offsets", seq_offsets, (S + 1) * 4}}))
+      return rc;
     ep::RouterArgs a{logits, select_bias, token_mask, seq_offsets, num_tokens, num_experts, topk,
                      num_sequences, dtype == EP_FP32, scoring == EP_SIGMOID, normalize != 0,
                      given != 0, scale, topk_idx, topk_weights, counts, seq_tokens, balance_loss,
@@ -1054,9 +1069,18 @@ int ep_router_backward(const void *logits, const int32_t *topk_idx, const int32_
     if (!aligned(logits, 16) || !aligned(d_logits, 16) || !aligned(topk_idx, 4) ||
         !aligned(d_topk_weights, 4) || !aligned(d_balance_loss, 4) || !aligned(d_z_loss, 4))
       return fail(EP_EINVAL, "%s: misaligned pointer (logits need 16 bytes)", what);
-    const int64_t bytes = (int64_t)num_tokens * num_experts * (dtype == EP_FP32 ? 4 : 2);
-    if (overlap(d_logits, bytes, logits, bytes))
-      return fail(EP_EINVAL, "%s: d_logits must not overlap logits", what);
+    const int64_t T = num_tokens, E = num_experts, S = num_sequences;
+    const int64_t bytes = T * E * (dtype == EP_FP32 ? 4 : 2);
+    if (int rc = check_apart(what, {{"d_logits", d_logits, bytes}},
+                             {{"logits", logits, bytes},
+                              {"topk_idx", topk_idx, T * topk * 4},
+                              {"seq_offsets", seq_offsets, (S + 1) * 4},
+                              {"counts", counts, S * E * 4},
+                              {"seq_tokens", seq_tokens, (S + 2) * 4},
+                              {"d_topk_weights", d_topk_weights, T * topk * 4},
+                              {"d_balance_loss", d_balance_loss, 4},
+                              {"d_z_loss", d_z_loss, 4}}))
+      return rc;
     ep::RouterBackwardArgs a{logits, topk_idx, seq_offsets, counts, seq_tokens, d_topk_weights,
                              d_balance_loss, d_z_loss, num_tokens, num_experts, topk, num_sequences,
                              dtype == EP_FP32, scoring == EP_SIGMOID, normalize != 0, scale,
