@@ -58,19 +58,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, in
 // 16 bytes per lane from memory to 1 KB of LDS at `to` (the same in every lane), lane after lane;
 // an offset outside the descriptor writes zeros. In assembly, because the compiler waits for every
 // load on its way before it reads LDS, whatever place the load writes: the waits are the kernel's own.
-// Nothing else here uses m0, which holds the place.
+// m0 holds the place. It is named as overwritten, so that the compiler keeps no value of its own there; that it
+// says that such a register is not restored is what is meant.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ uint32_t lds_at(const void *p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uintptr_t)(lds_void *)p);
 }
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
-               : "memory");
+               : "memory", "m0");
 }
 // The same with 4 bytes per lane, for scales.
 __device__ __forceinline__ void touch(__amdgpu_buffer_rsrc_t from, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const f32x2 f = {lo, hi};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
