@@ -37,7 +37,7 @@ constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
 // Reductions over a row's L lanes (16 or 64; the same result in each of them). Within 16 lanes by DPP
-// rotations. Every lane of the wave takes part: nothing here may be called by some lanes only.
+// rotations, which stay there: all of a row's lanes have to take part, and the four rows of a wave may differ.
 template <int N>
 __device__ __forceinline__ int rotate(int v) {  // by N within 16 lanes
   constexpr int kRowRor = 0x120;
@@ -653,8 +653,10 @@ __global__ __launch_bounds__(kThreads) void ep_router_sequences(const RouterArgs
     }
   }
   if (threadIdx.x == 0) {
-    // What this thread has published has left for all when its stores are done; there is nothing else to hand
-    // over, so no write-back of L2 (which takes 2.7 of 10.3 us for 37 sequences).
+    // What this thread has published has left for all when its stores are done, on this chip: relaxed stores of agent
+    // scope are written through, and this wait is for them. That is no order of the memory model, and holds for this
+    // thread's published values only: a value that the last workgroup is to read from other threads (a.counts, say)
+    // needs a release here, with its write-back of L2 (2.7 of 10.3 us for 37 sequences).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     last = __hip_atomic_fetch_add(in.done, (unsigned)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + (unsigned)mine == (unsigned)units;
   }
