@@ -689,6 +689,7 @@ __global__ __launch_bounds__(kThreads) void ep_router_backward_rows(const Router
   float *const mine = extra[group];
 #pragma unroll
   for (int j = 0; j < V; ++j) mine[column<L, V>(i, j)] = 0.f;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // other lanes add to these columns
   const float db = a.d_balance != nullptr ? *a.d_balance : 0.f, dz = a.d_z != nullptr ? *a.d_z : 0.f;
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
     const int64_t row = step * kGroups + group;
