@@ -17,11 +17,13 @@
 // - Scales through LDS beside the operands, not from memory at the tile's end (25 against 10 us a tile).
 // - A tile's blocks of 32 rows alternate between the waves, so that few rows are shared out evenly, and absent
 //   ones cost no products.
-// Measured on MI355X: 8192^3 458 us (2400 TOP/s; a large library product of the same codes 2184), 64 experts of
-// 512 rows 890 (2160), 8 of 2048 rows, 4096 to 2048, 127 to 130 (2100 to 2160).
+// Measured on MI355X: 8192^3 461 us (2385 TOP/s; a large library product of the same codes 472), three pairs of
+// matrices in turn 484 (480); 64 experts of 512 rows, 7168 to 4096, 890 to 966 by the card, 8 of 2048 rows, 4096 to
+// 2048, 127 to 143 (2160 to 1930). Fewer tiles than compute units leave the others idle: one matrix of
+// 64 to 128 rows, 7168 to 4096, takes 55 and 57 us, of 256 to 2048 rows 70 to 73, and 4096 to 1024 25 to 45.
 //
 // Experts with up to 32 rows: their weights are read once, which HBM bounds; see few_rows. 64 experts of
-// 8 rows, 7168 to 4096, 314 us (6.0 TB/s), of 32 rows 355; one row 8.4 us with the host's time (the kernel 8.8
+// 8 rows, 7168 to 4096, 314 us (6.0 TB/s), of 32 rows 357; one row 8.3 us with the host's time (the kernel 8.8
 // under a trace). The border: 64 experts of 32 rows 355 us there and 380 in tiles, and with up to 128
 // rows in parts of 32 496 to 918 us against 386 to 435 in tiles.
 #include <type_traits>
@@ -288,8 +290,12 @@ __device__ __forceinline__ void few_rows(const QuantizedMatmulArgs &a, FewLds &l
 // units of those with few. A unit takes 64 channels where that makes one for every workgroup, else 16
 // (7168 to 4096, 4 experts of 20 rows 27 against 34 us, of one row 23 against 26; from two or four on: no better).
 // When there are fewer tiles than workgroups, the others take kBeside units of 64 channels each in the
-// meantime, and the second launch begins behind those (128 tokens, top-8 of 64 experts by Zipf: 381 us
-// without, 363, 351, 339, 357 and 365 with 3, 4, 6, 8 and 10; both kinds shared out in one launch 400).
+// meantime, and the second launch begins behind those. Top-8 of 64 experts by Zipf, without and with 3, 4, 6, 8 and 10:
+//   128 tokens, 7168 -> 4096  378  364 352 340 351 362 us (128 tiles)
+//   64 tokens, 7168 -> 4096   381  352 340 331 328 334    (32 to 64 tiles)
+//   128 tokens, 2048 -> 7168  224  225 220 229 240 250    (196 to 224 tiles)
+//   top-4 of 32 experts, 4096 -> 2048  106  79 68 67 68 68 (32 to 40 tiles)
+// Both sides' times grow with the long axis, so the number does not go by it. Both kinds shared out in one launch: 400.
 constexpr int kBeside = 6;
 struct Plan {
   int tiles, rows, units, early, idle;  // rows: the most of an expert with few

@@ -13,11 +13,13 @@
 //
 // A row lies in 16 lanes (up to 256 experts; else in 64), so that a wave works on four at once and a
 // maximum over a row takes four DPP steps. What bounds it: for few tokens the launch (128 tokens of 256 experts,
-// 6.8 us under a trace, 8 with the host's time); for many the chain of a row's dependent steps, ten maxima of
-// which each needs the last, at four waves a SIMD. Measured on MI355X, 256 experts, top-8, fp32 logits:
-// 32768 tokens without statistics 15.2 us (softmax), 21 (sigmoid + bias); with them 33 and, in 37 packed
-// sequences, 43 (36 and 7.6 in the two launches); 4096 tokens 16.2. Backward 17 and 21 us, 131072 tokens 54
-// (5.0 TB/s, which is HBM). Steps: binary64 keys throughout 57 us for 128 tokens; statistics kept by workgroups of
+// 7 us under a trace, 8.5 with the host's time); for many the chain of a row's dependent steps, ten maxima of
+// which each needs the last, at four waves a SIMD. Measured on MI355X, top-8 of 32768 tokens of 256 experts, fp32
+// logits: without statistics 14.7 us (softmax), 20 (with a bias); with them 32 and, in 37 packed sequences, 43 to 47
+// (37 and 7 in the two launches), of 1024 experts 96 to 102; of given ids 22. 4096 tokens 15.7. Backward 17 and 20.5
+// us, 131072 tokens 58 (4.7 TB/s). Rows by the exact choice cost more: logits that are bf16 values (see Chooser) 46
+// us without statistics and 92 with, top-16 of 256 experts 175 and top-32 340 (candidates for 16 lanes only). Steps:
+// binary64 keys throughout 57 us for 128 tokens; statistics kept by workgroups of
 // 1024 threads, whose registers spill, 144 against 65 us; candidates ranked again one maximum at a time in
 // the rare near ties 77 against 20.6 us, since one such row holds up the launch.
 #include <type_traits>
@@ -210,9 +212,12 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 // maximum m on top. bf16 logits fit whole. Of binary32 keys the lower bits are lost: then K + 2
 // candidates (K + 4 of scores + bias) are taken and ranked by their whole keys, and the choice stands if what
 // was left out lies below the K-th whatever its lower bits are. Candidates' scores + bias that differ by no
-// more than their rounding errors (one row in a thousand) are ranked again in binary64. With K + 2 of them one
-// batch of 32768 tokens in two has a row that needs the exact choice, which holds up the launch (packed batch
-// 44 us without such a row, 56 to 90 with one); K + 4 cost 1 us and leave none.
+// more than their rounding errors (one row in a thousand) are ranked again in binary64. With K + 2 of scores + bias
+// one batch of 32768 tokens in two has a row that needs the exact choice, which holds up the launch (packed batch
+// 44 us without such a row, 56 to 90 with one); K + 4 cost 1 us and left none in 8 batches of drawn logits and
+// biases. Keys that are often equal need it more: binary32 logits that hold bf16 values, where three equal ones
+// around the last place leave too few candidates although no bits are lost (about 175 of 32768 rows of 256 experts,
+// 14.7 -> 46 us; with a bias of zeros 20 -> 37; of bf16 logits, 12.0, and continuous binary32 ones none).
 // Exact: binary64 keys, one maximum at a time; for rows where what is left out may reach the K-th (many
 // equal keys), for softmax + bias of rows that hold NaN or +infinity, and for more candidates than lanes.
 template <int L, int V>

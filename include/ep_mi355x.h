@@ -723,7 +723,9 @@ int ep_quantize_rows(const void *x, const int32_t *counts, const int32_t *offset
  * The experts' gated activation, quantised: ep_quantize_rows of
  *   h = gate / (1 + exp(-gate)) * up
  * in binary32 (gates below -87 as in ep_swiglu), h not rounded to the rows'
- * type in between.
+ * type in between. A code is that of h as binary32 rounds it: where h lies
+ * between two codes (one in a million) it may be the other neighbour of what
+ * exact arithmetic gives.
  *
  *   gate_up     [capacity_rows, 2 * intermediate] of dtype (EP_BF16, EP_FP32)
  *   codes       int8 [capacity_rows, intermediate]
